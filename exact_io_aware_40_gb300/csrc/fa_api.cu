@@ -11,6 +11,7 @@
 
 #include "fa.h"
 #include "kernels.h"
+#include "kv4.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -67,6 +68,10 @@ namespace {
 // One error word per device, written by kernels that give up on a stalled
 // pipeline; read and cleared by fa_check_error.
 __device__ int g_fa_error_word;
+// Written by the cache's kernels when a slot, page id or offset they read is
+// out of range.  A word of its own: a set error word ends the waits of every
+// kernel, and bad data of one call is no reason to stop another.
+__device__ int g_fa_input_word;
 
 constexpr int kMaxDevices = 64;
 
@@ -78,6 +83,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 
 std::mutex g_mu;
 int* g_err_ptr[kMaxDevices] = {};
+int* g_input_ptr[kMaxDevices] = {};
 unsigned long long g_err_ctx[kMaxDevices] = {};
 EncodeTiledFn g_encode = nullptr;
 
@@ -95,12 +101,21 @@ fa_status error_word(int dev, int** out) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_err_ptr[dev] == nullptr || g_err_ctx[dev] != ctx) {
     void* p = nullptr;
+    void* in = nullptr;
     if (cudaGetSymbolAddress(&p, g_fa_error_word) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaGetSymbolAddress(&in, g_fa_input_word) != cudaSuccess) return FA_ERR_CUDA;
     g_err_ptr[dev] = static_cast<int*>(p);
+    g_input_ptr[dev] = static_cast<int*>(in);
     g_err_ctx[dev] = ctx;
   }
   *out = g_err_ptr[dev];
   return FA_OK;
+}
+
+// The same for the word of input errors; valid after error_word(dev) succeeded.
+int* input_word(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_input_ptr[dev];
 }
 
 fa_status encoder(EncodeTiledFn* out) {
@@ -169,6 +184,23 @@ fa_status check_common(int B, int H, int N, int d, float scale) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+namespace fa {
+
+int error_words(ErrorWords* out) {
+  int dev;
+  fa_status st = current_device(&dev);
+  if (st != FA_OK) return st;
+  if ((st = error_word(dev, &out->wait)) != FA_OK) return st;
+  out->input = input_word(dev);
+  return FA_OK;
+}
+
+}  // namespace fa
+
+namespace {
 
 // A pipeline stage whose producer never arrives: every thread of one CTA waits
 // on an mbarrier that nothing signals, through the same bounded wait the
@@ -575,13 +607,20 @@ fa_status fa_check_error(fa_stream_t stream) {
   int host = 0;
   if (cudaMemcpy(&host, err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return FA_ERR_CUDA;
+  int* in = input_word(dev);
+  int bad_input = 0;
+  if (cudaMemcpy(&bad_input, in, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return FA_ERR_CUDA;
+  const int zero = 0;
+  if (bad_input != 0 &&
+      cudaMemcpy(in, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+    return FA_ERR_CUDA;
   if (host != 0) {
-    const int zero = 0;
     if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
       return FA_ERR_CUDA;
     return host == FA_ERR_TIMEOUT ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
   }
-  return FA_OK;
+  return bad_input != 0 ? FA_ERR_INVALID_ARG : FA_OK;
 }
 
 }  // extern "C"

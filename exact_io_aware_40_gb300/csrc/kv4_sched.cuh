@@ -1,0 +1,193 @@
+// kv4_sched.cuh -- how attention over the paged cache is dealt out to CTAs.
+//
+// The work is a list of items: request b, block rb of its query rows, K/V head
+// h.  A request's rows are its n queries times the per_kv query heads that
+// share a K/V head (row = query * per_kv + head in the group), so that a tile of
+// the cache that was read once serves all of them.  An item is a run of
+// 64-token tiles, those that hold a key visible to one of its rows (at least
+// one, so that a block that sees nothing still writes its zeros).  All tiles of
+// all items form one list which is cut into equal shares, one per CTA: lengths
+// may differ by any factor and the shares do not.  An item that a share's end
+// cuts is finished from partial results (kv4_merge.cu).
+#pragma once
+#include "kv4.h"
+
+namespace fa {
+
+constexpr int kKv4Tile = 64;
+
+struct Kv4Req {
+  int start, n, kv;  // first row of Q, queries, keys
+};
+
+__device__ __forceinline__ Kv4Req kv4_request(const Kv4AttnArgs& a, int b, bool* bad) {
+  const int start = a.cu_q[b], end = a.cu_q[b + 1];
+  Kv4Req r;
+  r.start = start;
+  r.n = end - start;
+  if (start < 0 || end < start || end > a.total_q || r.n > a.max_q) {
+    r.n = 0;
+    *bad = true;
+  }
+  const long long room = static_cast<long long>(a.max_pages) << a.lay.page_shift;
+  r.kv = static_cast<int>(min(static_cast<long long>(max(a.kv_len[b], 0)), room));
+  return r;
+}
+
+struct Kv4Block {
+  int row0, rows;         // rows of the block
+  int pos0;               // position of the request's first query
+  int lo, hi;             // keys that some row sees
+  int all_lo, all_hi;     // keys that every row sees
+  int tile_lo, tiles;
+};
+
+__device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req& r, int rb,
+                                              int block_rows) {
+  Kv4Block k;
+  k.row0 = rb * block_rows;
+  k.rows = min(r.n * a.per_kv - k.row0, block_rows);
+  k.pos0 = r.kv - r.n;
+  const int first = k.row0 / a.per_kv, last = (k.row0 + k.rows - 1) / a.per_kv;
+  k.lo = 0;
+  k.hi = r.kv;
+  k.all_lo = 0;
+  k.all_hi = r.kv;
+  if (a.causal || a.window >= 0) {
+    k.hi = max(min(r.kv, k.pos0 + last + 1), 0);
+    k.all_hi = max(k.pos0 + first + 1, 0);
+  }
+  if (a.window >= 0) {
+    // p - w, without passing the range of int for a large window
+    k.lo = max(k.pos0 + first - min(a.window, 0x3fffffff), 0);
+    k.all_lo = max(k.pos0 + last - min(a.window, 0x3fffffff), 0);
+  }
+  k.tile_lo = k.lo / kKv4Tile;
+  k.tiles = max((k.hi + kKv4Tile - 1) / kKv4Tile - k.tile_lo, 1);
+  return k;
+}
+
+__device__ __forceinline__ long long kv4_units(const Kv4AttnArgs& a, int b, int block_rows,
+                                               bool* bad) {
+  const Kv4Req r = kv4_request(a, b, bad);
+  const int blocks = (r.n * a.per_kv + block_rows - 1) / block_rows;
+  long long n = 0;
+  for (int rb = 0; rb < blocks; ++rb) n += kv4_block(a, r, rb, block_rows).tiles;
+  return n * a.Hkv;
+}
+
+struct Kv4Share {
+  long long total, per;  // tiles in the list, tiles a share
+  long long begin;       // first tile of the list that belongs to request b
+  int b;
+};
+
+// The whole block finds its share; `scratch` holds kThreads / 32 + 2 long longs.
+// Shares are at least min_tiles long.  begin/b are set when the share is not
+// empty (blockIdx.x * per < total).
+template <int kThreads>
+__device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_rows, int min_tiles,
+                                              long long* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  long long first = tid < a.B ? kv4_units(a, tid, block_rows, &bad) : 0;
+  long long sum = first;
+  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += kv4_units(a, b, block_rows, &bad);
+  if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  Kv4Share s;
+  s.total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) s.total += scratch[w];
+  s.per = max((s.total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
+  s.b = 0;
+  s.begin = 0;
+  const long long u0 = s.per * blockIdx.x;
+  if (u0 >= s.total) return s;
+  long long run = 0;
+  for (int base = 0; base < a.B; base += kThreads) {
+    const int b = base + tid;
+    long long v = first;
+    if (base) v = b < a.B ? kv4_units(a, b, block_rows, &bad) : 0;
+    long long incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    __syncthreads();  // the last reads of scratch are done
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = run;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    for (int w = 0; w < kThreads / 32; ++w) run += scratch[w];
+    if (u0 >= before + incl - v && u0 < before + incl) {
+      scratch[kThreads / 32] = before + incl - v;
+      scratch[kThreads / 32 + 1] = b;
+    }
+    if (run > u0) break;
+  }
+  __syncthreads();
+  s.begin = scratch[kThreads / 32];
+  s.b = static_cast<int>(scratch[kThreads / 32 + 1]);
+  return s;
+}
+
+// A CTA's walk through its share, item by item.
+struct Kv4Walk {
+  Kv4Req req;
+  Kv4Block blk;
+  int b, rb, h, blocks;
+  long long item;  // index in the list of the item's first tile
+
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a, int block_rows) {
+    bool bad = false;
+    req = kv4_request(a, b, &bad);
+    blocks = (req.n * a.per_kv + block_rows - 1) / block_rows;
+    rb = 0;
+    h = 0;
+    if (blocks) blk = kv4_block(a, req, 0, block_rows);
+  }
+  // To the item that holds tile u of the list, from the request that holds it.
+  __device__ __forceinline__ void seek(const Kv4AttnArgs& a, const Kv4Share& s, long long u,
+                                       int block_rows) {
+    b = s.b;
+    item = s.begin;
+    open(a, block_rows);
+    while (u >= item + static_cast<long long>(blk.tiles) * a.Hkv) {
+      item += static_cast<long long>(blk.tiles) * a.Hkv;
+      ++rb;
+      blk = kv4_block(a, req, rb, block_rows);
+    }
+    h = static_cast<int>((u - item) / blk.tiles);
+    item += static_cast<long long>(h) * blk.tiles;
+  }
+  __device__ __forceinline__ void next(const Kv4AttnArgs& a, int block_rows) {
+    item += blk.tiles;
+    if (++h < a.Hkv) return;
+    h = 0;
+    if (++rb < blocks) {
+      blk = kv4_block(a, req, rb, block_rows);
+      return;
+    }
+    while (++b < a.B) {
+      open(a, block_rows);
+      if (blocks) return;
+    }
+  }
+};
+
+// The record a CTA leaves for the merge: the item, cut by this share's end,
+// that begins in it (x: first query of its request, y: first row of its block,
+// z: rows + 256 * K/V head, 0: there is none, w: the last CTA with a part of
+// it).  Partial results of CTA i are number 2 i (of its first item, begun
+// before) and 2 i + 1 (of its last, begun here).
+__device__ __forceinline__ int4 kv4_split_record(const Kv4Walk& w, const Kv4Share& s) {
+  return make_int4(w.req.start, w.blk.row0, w.blk.rows + 256 * w.h,
+                   static_cast<int>((w.item + w.blk.tiles - 1) / s.per));
+}
+
+}  // namespace fa

@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/fa.h (libfa_sm103.so).
+"""ctypes binding of the C ABI in include/fa.h and include/fa_kv4.h (libfa_sm103.so).
 
 Argument marshalling only: every step of attention runs in the library's CUDA
 kernels.  Tensors are torch CUDA tensors (PyTorch provides device memory and
@@ -61,7 +61,17 @@ def load_library():
     lib.fa_check_error.argtypes = [vp]
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
-    for fn in ("fa_fwd", "fa_fwd_kvlen", "fa_fwd_masked", "fa_bwd", "fa_bwd_masked",
+    lib.fa_kv4_page_bytes.argtypes = [i, i, i]
+    lib.fa_kv4_page_bytes.restype = sz
+    lib.fa_kv4_plan.argtypes = [vp, vp, i, i, i, vp, i, vp, vp, i, vp, vp, vp, vp, vp]
+    lib.fa_kv4_append.argtypes = [vp, vp, i, i, i, i, i, i, i, vp, vp, i, i, i, vp]
+    lib.fa_kv4_gather.argtypes = [vp, vp, i, i, i, i, i, i, vp, vp, vp]
+    lib.fa_kv4_attn_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_kv4_attn_workspace_bytes.restype = sz
+    lib.fa_kv4_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i, i, i, f,
+                                i, i, vp, sz, vp]
+    for fn in ("fa_kv4_plan", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attn",
+               "fa_fwd", "fa_fwd_kvlen", "fa_fwd_masked", "fa_bwd", "fa_bwd_masked",
                "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_fp8",
                "fa_bwd_prepare", "fa_bwd_dkdv",
                "fa_bwd_dq", "fa_check_error", "fa_selftest_stalled_wait"):
@@ -327,6 +337,205 @@ def attention_bwd(q, k, v, o, do, L, causal=False, scale=None, kv_len=None, work
         else:
             fa_bwd(q, k, v, o, do, L, dq, dk, dv, scale, causal, kv_len, workspace, stream)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ paged 4-bit cache
+
+def kv4_page_bytes(d, page_size, group=32):
+    """Bytes of one page of one K/V head; raises for an unsupported geometry."""
+    n = int(load_library().fa_kv4_page_bytes(d, page_size, group))
+    if n == 0:
+        raise ValueError("d must be 64, 128 or 256, page_size 16, 32, 64 or 128 and group 32 or "
+                         "64, got %s, %s, %s" % (d, page_size, group))
+    return n
+
+
+def kv4_cache(num_pages, kv_heads, page_size, d, group=32, device="cuda"):
+    """A cache of num_pages pages: uint8 [num_pages, kv_heads, page bytes], uninitialised
+    (rows that were not appended are never used)."""
+    import torch
+    return torch.empty(num_pages, kv_heads, kv4_page_bytes(d, page_size, group), dtype=torch.uint8,
+                       device=device)
+
+
+def _expect_cache(cache, page_size, d, group):
+    """Checks a cache tensor against its geometry; returns (num_pages, kv_heads)."""
+    import torch
+    record = kv4_page_bytes(d, page_size, group)
+    if cache.dim() != 3:
+        raise ValueError("expected a [num_pages, kv_heads, page bytes] cache")
+    pages, heads = cache.shape[0], cache.shape[1]
+    _expect(cache, "cache", torch.uint8, (pages, heads, record))
+    return pages, heads
+
+
+def _expect_rows(t, name, shape):
+    """Checks a bf16 [tokens, heads, d] CUDA tensor; returns its token and head strides."""
+    import torch
+    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != shape or t.stride(2) != 1:
+        raise ValueError("%s must be a CUDA torch.bfloat16 tensor of shape %s with contiguous "
+                         "channels" % (name, shape))
+    ts, hs = (st if n > 1 else 0 for st, n in zip(t.stride()[:2], shape))
+    if ts % 8 or hs % 8 or max(ts, hs) > 0x7fffffff or t.data_ptr() % 16:
+        raise ValueError("%s: strides must be multiples of 8 elements (below 2^31) and the data "
+                         "16-byte aligned" % name)
+    return ts, hs
+
+
+def _expect_i32(t, name, shape):
+    import torch
+    _expect(t, name, torch.int32, shape)
+
+
+def _on_device(device, stream):
+    """Makes `device`, and `stream` if one is given, current for a call: what the call
+    allocates then belongs to the stream that uses it."""
+    import contextlib
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def kv4_plan(past_len, new_len, block_table, free_list, free_state, page_size, max_tokens,
+             num_pages=None, stream=None):
+    """One step's pages and slots from the requests' lengths, on the GPU (fa_kv4_plan).
+
+    past_len, new_len: CUDA int32 [B] (new_len -1: the request is finished); block_table int32
+    [B, max_pages] and free_list int32 [num_pages] are updated in place; free_state int32 [>= 2]
+    (first free entry, number): the state an earlier call returned.  Returns (kv_len [B],
+    cu_q [B + 1], slots [max_tokens], state [4])."""
+    import torch
+    B = past_len.numel()
+    if block_table.dim() != 2:
+        raise ValueError("expected a [B, max_pages] block_table")
+    max_pages = block_table.shape[1]
+    num_pages = free_list.numel() if num_pages is None else int(num_pages)
+    _expect_i32(past_len, "past_len", (B,))
+    _expect_i32(new_len, "new_len", (B,))
+    _expect_i32(block_table, "block_table", (B, max_pages))
+    _expect_i32(free_list, "free_list", (num_pages,))
+    _expect_i32(free_state, "free_state", (free_state.numel(),))
+    if free_state.numel() < 2:
+        raise ValueError("free_state must hold the first free entry and their number")
+    if max_tokens < 1:
+        raise ValueError("max_tokens must be positive")
+    _same_device(past_len, new_len, block_table, free_list, free_state)
+    dev = past_len.device
+    # one allocation; each part starts on a 16-byte boundary
+    r4 = lambda n: (n + 3) // 4 * 4
+    n_kv, n_cu, n_slots = r4(B), r4(B + 1), r4(max_tokens)
+    with _on_device(dev, stream):
+        out = torch.empty(n_kv + n_cu + n_slots + 4, dtype=torch.int32, device=dev)
+        kv_len, cu_q = out[:B], out[n_kv:n_kv + B + 1]
+        slots = out[n_kv + n_cu:n_kv + n_cu + max_tokens]
+        state = out[n_kv + n_cu + n_slots:]
+        _check(load_library().fa_kv4_plan(
+            _ptr(past_len), _ptr(new_len), B, page_size, num_pages, _ptr(block_table), max_pages,
+            _ptr(free_list), _ptr(free_state), max_tokens, _ptr(kv_len), _ptr(cu_q), _ptr(slots),
+            _ptr(state), _stream(stream, past_len)), "fa_kv4_plan")
+    return kv_len, cu_q, slots, state
+
+
+def kv4_append(k, v, slots, cache, page_size, group=32, stream=None):
+    """Quantises k, v (bf16 [T, kv_heads, d], views of a packed projection allowed) and writes
+    them to their slots (CUDA int32 [T], -1 skips) in the cache (fa_kv4_append)."""
+    if k.dim() != 3:
+        raise ValueError("expected [T, kv_heads, d] keys and values")
+    T, heads, d = (int(x) for x in k.shape)
+    pages, cache_heads = _expect_cache(cache, page_size, d, group)
+    if heads != cache_heads:
+        raise ValueError("k has %d heads, the cache %d" % (heads, cache_heads))
+    k_ts, k_hs = _expect_rows(k, "k", (T, heads, d))
+    v_ts, v_hs = _expect_rows(v, "v", (T, heads, d))
+    _expect_i32(slots, "slots", (T,))
+    _same_device(k, v, slots, cache)
+    if T == 0:
+        return
+    with _on_device(cache.device, stream):
+        _check(load_library().fa_kv4_append(
+            _ptr(k), _ptr(v), T, heads, d, k_ts, k_hs, v_ts, v_hs,
+            _ptr(slots), _ptr(cache), pages, page_size, group, _stream(stream, cache)),
+            "fa_kv4_append")
+
+
+def kv4_gather(slots, cache, page_size, d, group=32, out_k=None, out_v=None, stream=None):
+    """The values the cache holds at `slots` (CUDA int32 [T]): bf16 (K, V), each
+    [T, kv_heads, d].  Rows whose slot is -1 are not written (fa_kv4_gather)."""
+    import torch
+    pages, heads = _expect_cache(cache, page_size, d, group)
+    T = slots.numel()
+    _expect_i32(slots, "slots", (T,))
+    shape = (T, heads, d)
+    _same_device(slots, cache, out_k, out_v)
+    with _on_device(cache.device, stream):
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        _expect(out_k, "out_k", torch.bfloat16, shape)
+        _expect(out_v, "out_v", torch.bfloat16, shape)
+        if T:
+            _check(load_library().fa_kv4_gather(
+                _ptr(slots), _ptr(cache), pages, page_size, group, T, heads, d, _ptr(out_k),
+                _ptr(out_v), _stream(stream, cache)), "fa_kv4_gather")
+    return out_k, out_v
+
+
+def kv4_attention_workspace_bytes(q_heads, kv_heads, d, max_q):
+    return int(load_library().fa_kv4_attn_workspace_bytes(q_heads, kv_heads, d, max_q))
+
+
+def kv4_attention(q, cache, block_table, cu_q, kv_len, max_q, page_size, group=32, causal=True,
+                  scale=None, window=-1, out=None, lse=None, workspace=None, stream=None):
+    """Exact attention of new tokens over the cache (fa_kv4_attn).
+
+    q: bf16 [total_q, q_heads, d], the requests' new tokens one after the other (views of a
+    packed projection allowed); block_table int32 [B, max_pages]; cu_q int32 [B + 1] (request b
+    has rows cu_q[b] .. cu_q[b + 1] - 1, at most max_q of them, its last tokens); kv_len int32
+    [B], new tokens included.  Query heads h * q_heads / kv_heads .. share K/V head h.  Returns
+    (O bf16 [total_q, q_heads, d], L fp32 [total_q, q_heads]); rows behind the last request are
+    not written."""
+    import torch
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("expected [total_q, q_heads, d] queries and a [B, max_pages] block_table")
+    total, q_heads, d = (int(x) for x in q.shape)
+    pages, kv_heads = _expect_cache(cache, page_size, d, group)
+    B, max_pages = (int(x) for x in block_table.shape)
+    q_ts, q_hs = _expect_rows(q, "q", (total, q_heads, d))
+    if q_heads % kv_heads:
+        raise ValueError("%d query heads do not divide into %d K/V heads" % (q_heads, kv_heads))
+    _expect_i32(block_table, "block_table", (B, max_pages))
+    _expect_i32(cu_q, "cu_q", (B + 1,))
+    _expect_i32(kv_len, "kv_len", (B,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is not None:
+        _expect(out, "out", torch.bfloat16, (total, q_heads, d))
+    if lse is not None:
+        _expect(lse, "lse", torch.float32, (total, q_heads))
+    if workspace is not None:
+        _expect(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    _same_device(q, cache, block_table, cu_q, kv_len, out, lse, workspace)
+    dev = q.device
+    with _on_device(dev, stream):
+        if out is None:
+            out = torch.empty((total, q_heads, d), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((total, q_heads), dtype=torch.float32, device=dev)
+        if total == 0 or B == 0:
+            return out, lse
+        if workspace is None:
+            workspace = torch.empty(kv4_attention_workspace_bytes(q_heads, kv_heads, d, max_q),
+                                    dtype=torch.uint8, device=dev)
+        _check(load_library().fa_kv4_attn(
+            _ptr(q), _ptr(cache), _ptr(block_table), _ptr(cu_q), _ptr(kv_len), _ptr(out),
+            _ptr(lse), B, total, max_q, q_heads, kv_heads, d, q_ts, q_hs, pages, max_pages,
+            page_size, group, float(scale), int(bool(causal)), int(window), _ptr(workspace),
+            workspace.numel(), _stream(stream, q)), "fa_kv4_attn")
+    return out, lse
 
 
 # ------------------------------------------------------------------ autograd

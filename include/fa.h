@@ -30,8 +30,8 @@
  *     every query of batch b; values are clamped to [0, N].  A query with no
  *     visible key gets O = 0, L = -inf and zero gradients.
  *   - Ownership: the caller owns every buffer.  The library allocates no device
- *     memory in these calls; its only device state is one 4-byte error word per
- *     device (a static device variable).
+ *     memory in these calls; its only device state is two 4-byte error words per
+ *     device (static device variables).
  *   - Asynchrony: every call only enqueues work on `stream` (NULL = the legacy
  *     default stream) and returns; nothing synchronises except
  *     fa_check_error().
@@ -269,7 +269,8 @@ fa_status fa_selftest_stalled_wait(uint64_t limit_ns, fa_stream_t stream);
 /*
  * Synchronises `stream`, then returns and clears the current device's error
  * word (FA_ERR_TIMEOUT if a kernel gave up), or FA_ERR_CUDA if the stream
- * itself reports an error.
+ * itself reports an error.  FA_ERR_INVALID_ARG: a kernel of fa_kv4.h met data
+ * out of its range.
  */
 fa_status fa_check_error(fa_stream_t stream);
 
