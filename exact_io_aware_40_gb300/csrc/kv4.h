@@ -78,12 +78,12 @@ struct Kv4AttnArgs {
   Kv4Layout lay;
   float scale_log2;  // scale * log2(e)
   int causal, window;
+  int whole_items;   // items are not cut (kv4_sched.cuh)
   int *wait_err, *input_err;
   // workspace: one Kv4Split per CTA, then per CTA two partial results of
-  // `rows` query rows: statistics (m, l, l of the rounded weights, unused)
-  // and fp32 O
+  // `rows` query rows: statistics (m, l) and fp32 O
   int4* split;
-  float4* part_stat;
+  float2* part_stat;
   float* part_o;
 };
 

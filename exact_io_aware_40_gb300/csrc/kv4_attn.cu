@@ -2,9 +2,9 @@
 //
 // Up to 32 rows (queries x query heads of one K/V head) share each read of the
 // cache; one read of the keys and values is all the memory traffic there is, so
-// the kernel is built around it: a warp walks the cache on its own, 16 tokens at
+// the kernel is built around it: a warp walks the cache on its own, 32 tokens at
 // a time, with its copies (cp.async) several steps ahead and no barrier with any
-// other warp until its item ends.  Per step of 16 tokens and a K/V head:
+// other warp until its item ends.  Per 16 tokens and a K/V head:
 //
 //   S^T = K Q^T   mma m16n8k16, A = 16 tokens x 16 channels of codes, B = Q^T
 //   p   = 2^(S scale log2e - m), running maximum m and sums in fp32
@@ -13,18 +13,24 @@
 // Tokens (then channels) are the 16 rows of the product and query rows its 8
 // columns, so one to eight rows cost one product.
 //
-// Codes become bf16 without a conversion: 0x4300 | c is 128 + c.  For K that is
-// all: per group of channels sum q (m + s c) = s sum q (128 + c) + (m - 128 s)
-// sum q, two FMAs per score on exact products.  128 exceeds the codes by a
-// factor of 8 to 128, which costs 7 of fp32's 24 bits at most.  For V, 128 is
-// subtracted (exact) and one bf16 FMA gives the value rounded to bf16, as if V
-// had been a bf16 tensor; P is rounded to bf16 as in the bf16 forward.  O is
-// divided by the sum of the rounded weights, L uses the unrounded ones.
+// Codes become numbers without a conversion.  K: 0x4300 | c is 128 + c in bf16,
+// and per group of channels sum q (m + s c) = s sum q (128 + c) + (m - 128 s)
+// sum q, two FMAs per score on exact products; 128 exceeds the codes by a factor
+// of 8 to 128, which costs 7 of fp32's 24 bits at most.  V: 0x6400 | c is 1024 +
+// c and 0x6400 | 16 c is 1024 + 16 c in fp16; one exact operation makes c - 8 of
+// either, one FMA the value.  (An offset as K's is no choice here: the values
+// average out over a long context and the offset would not.)  V and P are fp16
+// in the product, which rounds them to 2^-12 where bf16 has 2^-9, so that the
+// rounding of O to bf16 is what is left; the price is a scale.  V is taken in
+// units of 2^vexp, a power of two that grows with the largest value met (as the
+// running maximum does), P in units of 2^-kShift of the maximum's weight:
+// weights below 2^-34 of it and values below 2^-38 of the largest one are lost.
 //
 // Which token is which row of the product is free as long as both products
-// agree; kTokenOf and the swizzle of the 16-byte chunks (chunk_of) are chosen so
-// that a warp's reads of its staged codes touch every bank once.
-#include <cuda_bf16.h>
+// agree; token_of and the swizzle of the staged 16-byte chunks (twist) are chosen
+// so that a warp's reads of its staged codes meet no bank twice (K), or twice
+// at most (V).
+#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -38,9 +44,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr int kStepTokens = 16;
-static_assert(kWarps * kStepTokens == kKv4Tile, "a tile is one step of every warp");
-constexpr float kGrow = 8.f;  // log2 units: m moves only when the maximum passes it by more
+constexpr int kStepTokens = 32;
+constexpr int kTile = kWarps * kStepTokens;  // one step of every warp
+constexpr float kGrow = 4.f;    // log2 units: m moves only when the maximum passes it by more
+constexpr float kShift = 10.f;  // P is at most 2^(kGrow + kShift)
 constexpr float kLn2f = 0.693147180559945309f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -51,10 +58,18 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -64,29 +79,71 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t keep, uint32_t set) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(keep), "r"(set));
   return r;
 }
 // Nibbles i and i + 4 of w as bf16 values 128 + code.
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t k_codes(uint32_t w, int i) {
+  return and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
 }
+// Nibbles i and i + 4 of w as fp16 values code - 8.
+__device__ __forceinline__ uint32_t v_codes(uint32_t w, int i) {
+  const uint32_t x = i < 2 ? w : w >> 8;
+  if ((i & 1) == 0) return add_f16x2(and_or(x, 0x000f000fu, 0x64006400u), 0xe408e408u);  // -1032
+  return fma_f16x2(and_or(x, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+}
+__device__ __forceinline__ bool odd_param(uint32_t p) {  // NaN or infinity in either half
+  return (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float param_min(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
-// Token (of a step's 16) that is row r of the product.
+// Token (of 16) that is row r of the product.
 __device__ __forceinline__ int token_of(int r) { return (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3); }
 
+// The 16-byte chunks of a staged row of codes are permuted by an XOR with this.
 template <int HD>
-__device__ __forceinline__ int chunk_of(int tok, int chunk) {  // 16-byte chunk of a staged row
-  if (HD == 64) return chunk ^ ((tok >> 2) & 1);
-  if (HD == 128) return chunk ^ ((tok & 2) | ((tok >> 2) & 1));
-  return chunk ^ (((tok << 1) | ((tok >> 2) & 1)) & 7);
+__device__ __forceinline__ int twist(int tok) {
+  if (HD == 64) return (tok >> 2) & 1;
+  if (HD == 128) return (tok & 2) | ((tok >> 2) & 1);
+  return ((tok << 1) | ((tok >> 2) & 1)) & 7;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+  }
 }
 
 template <int HD, int GROUP, int NT>
@@ -95,7 +152,8 @@ struct AttnCfg {
   static constexpr int kCodeRow = HD / 2, kParamRow = 4 * kGroups;
   static constexpr int kCodes = kStepTokens * kCodeRow, kParams = kStepTokens * kParamRow;
   static constexpr int kStage = 2 * (kCodes + kParams);  // bytes: K codes, V codes, K, V params
-  static constexpr int kStages = HD == 64 ? 6 : 4;
+  static_assert(kStage % 128 == 0, "the swizzle works on addresses");
+  static constexpr int kStages = HD == 64 ? 4 : HD == 128 ? (NT == 4 ? 4 : 2) : 2;
   static constexpr int kStageBytes = kWarps * kStages * kStage;
   static constexpr int kMergeBytes = kWarps * 8 * HD * 4;  // 8 rows of every warp's O
   static constexpr int kSmem = kStageBytes > kMergeBytes ? kStageBytes : kMergeBytes;
@@ -110,72 +168,101 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   using C = AttnCfg<HD, GROUP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scratch[kWarps + 2];
-  __shared__ float stat[3][kWarps][C::kRows];
+  __shared__ float stat[2][kWarps][C::kRows];
+  // The merge may be launched; it waits for this grid's end by itself.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q = lane & 3;  // row / column pair of the product's fragments
 
-  const Kv4Share share = kv4_share<kAttnThreads>(a, C::kRows, 2, scratch);
+  const Kv4Share share = kv4_share<kTile, kAttnThreads>(a, C::kRows, 1, scratch);
   long long u = share.per * blockIdx.x;
   const long long u_end = min(share.total, u + share.per);
   if (tid == 0 && u >= share.total) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (u >= share.total) return;
   bool first_item = true;
-  Kv4Walk w;
+  Kv4Walk<kTile> w;
   w.seek(a, share, u, C::kRows);
   const uint8_t* stage0 = smem + warp * C::kStages * C::kStage;
   const uint32_t stage0_u32 = smem_u32(stage0);
   int4 record = make_int4(0, 0, 0, 0);
 
-  for (; u < u_end; w.next(a, C::kRows)) {
-    const int ta = static_cast<int>(u - w.item);
-    const int tb = static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
-    const int steps = tb - ta;
-    const int tok0 = (w.blk.tile_lo + ta) * kKv4Tile + warp * kStepTokens;
+  // Lane constants of the staged layout.
+  const int t0 = token_of(r);  // K, P: rows r and r + 8 are tokens t0 and t0 + 8
+  const int k_at = t0 * C::kCodeRow + twist<HD>(t0) * 16 + q * 4;
+  const int kp_at = 2 * C::kCodes + t0 * C::kParamRow;
+  int v_at[2], vp_at[2];       // V: tokens ta[e] and ta[e] + 8 of this lane's columns
+  int ta[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    ta[e] = token_of(2 * q + e);
+    const int byte = r * (HD / 16);
+    v_at[e] = C::kCodes + ta[e] * C::kCodeRow + (((byte >> 4) ^ twist<HD>(ta[e])) << 4) + (byte & 15);
+    vp_at[e] = 2 * C::kCodes + C::kParams + ta[e] * C::kParamRow + (r * (HD / 8)) / GROUP * 4;
+  }
+  // Copies: chunk lane of a half step's codes (16 tokens), and of its params.
+  const int cp_tok = (lane * 16) / C::kCodeRow;
+  const uint32_t cp_dst =
+      cp_tok * C::kCodeRow + ((((lane * 16) % C::kCodeRow >> 4) ^ twist<HD>(cp_tok & 7)) << 4);
 
-    // ------------------------------------------------ copies, S - 1 steps ahead
-    int page = -1, page_next = -1;  // lane l: page of step 32 k + l
-    uint32_t live = 0;              // bit i % 32: step i has something to do
+  for (; u < u_end; w.next(a, C::kRows)) {
+    const int first_tile = static_cast<int>(u - w.item);
+    const int last_tile =
+        a.whole_items ? w.blk.tiles
+                      : static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
+    const int tok0 = (w.blk.tile_lo + first_tile) * kTile + warp * kStepTokens;
+    // Steps of this warp that hold a key some row sees.
+    const int steps =
+        min(last_tile - first_tile, max(0, (w.blk.hi - tok0 + kTile - 1) / kTile));
+
+    // ------------------------------------------------ copies, kStages - 1 steps ahead
+    int page = 0, page_next = 0;  // lane l: page of half l % 2 of step 16 k + l / 2
     auto fetch_page = [&](int i) -> int {
-      const int tok = tok0 + (i + lane) * kKv4Tile;
-      if (i + lane >= steps || tok >= w.blk.hi) return -1;
-      return __ldg(a.table + static_cast<long long>(w.b) * a.max_pages + (tok >> a.lay.page_shift));
+      const int tok = tok0 + (i + (lane >> 1)) * kTile + (lane & 1) * 16;
+      if (i + (lane >> 1) >= steps || tok >= w.blk.hi) return 0;
+      const int p = __ldg(a.table + static_cast<long long>(w.b) * a.max_pages +
+                          (tok >> a.lay.page_shift));
+      if (p >= 0 && p < a.num_pages) return p;
+      atomicCAS(a.input_err, 0, 1);
+      return 0;
     };
     page_next = fetch_page(0);
+    const uint8_t* head_base = a.cache + static_cast<long long>(w.h) * a.lay.record;
+    const long long page_bytes = static_cast<long long>(a.Hkv) * a.lay.record;
     auto issue = [&](int i) {
       if (i < steps) {
-        if ((i & 31) == 0) {
+        if ((i & 15) == 0) {
           page = page_next;
-          page_next = fetch_page(i + 32);
+          page_next = fetch_page(i + 16);
         }
-        const int pg = __shfl_sync(0xffffffffu, page, i & 31);
-        const int tok = tok0 + i * kKv4Tile;
-        bool ok = tok < w.blk.hi;
-        if (ok && (pg < 0 || pg >= a.num_pages)) {
-          if (lane == 0) atomicCAS(a.input_err, 0, 1);
-          ok = false;
-        }
-        live = (live & ~(1u << (i & 31))) | (ok ? 1u << (i & 31) : 0u);
-        if (ok) {
+        const uint32_t dst = stage0_u32 + (i % C::kStages) * C::kStage;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int tok = tok0 + i * kTile + hf * 16;
+          const int pg = __shfl_sync(0xffffffffu, page, 2 * (i & 15) + hf);
+          if (hf && tok >= w.blk.hi) break;  // nothing there: left as it is, and masked
           const int off = tok & ((1 << a.lay.page_shift) - 1);
-          const uint8_t* rec =
-              a.cache + (static_cast<long long>(pg) * a.Hkv + w.h) * a.lay.record;
-          const uint8_t* kc = rec + off * C::kCodeRow;
+          const uint8_t* rec = head_base + pg * page_bytes;
+          const uint8_t* kc = rec + off * C::kCodeRow + lane * 16;
           const uint8_t* vc = kc + a.lay.v_codes;
-          const uint32_t dst = stage0_u32 + (i % C::kStages) * C::kStage;
-          constexpr int kChunks = HD / 32;  // 16-byte chunks of a row of codes
 #pragma unroll
-          for (int k = lane; k < C::kCodes / 16; k += 32) {
-            const int t = k / kChunks, c = k % kChunks;
-            const uint32_t at = dst + (t * kChunks + chunk_of<HD>(t & 7, c)) * 16;
-            cp_async16(at, kc + k * 16);
-            cp_async16(at + C::kCodes, vc + k * 16);
+          for (int j = 0; j < HD / 64; ++j) {
+            // 512 bytes are 16, 8 or 4 rows on; 4 rows change the twist's low bit
+            const uint32_t at = dst + hf * 16 * C::kCodeRow + j * 512 +
+                                (HD == 256 && (j & 1) ? cp_dst ^ 16u : cp_dst);
+            cp_async16(at, kc + j * 512);
+            cp_async16(at + C::kCodes, vc + j * 512);
           }
-          constexpr int kP = C::kParams / 16;
-          const uint8_t* kp = rec + a.lay.k_params + off * C::kParamRow;
-          const uint8_t* vp = rec + a.lay.v_params + off * C::kParamRow;
-#pragma unroll
-          for (int k = lane; k < 2 * kP; k += 32)
-            cp_async16(dst + 2 * C::kCodes + k * 16, (k < kP ? kp + k * 16 : vp + (k - kP) * 16));
+          constexpr int kP = C::kParamRow;  // 16-byte chunks of 16 tokens' params
+          const uint32_t pat = dst + 2 * C::kCodes + hf * 16 * kP;
+          const uint8_t* kp = rec + a.lay.k_params + off * kP;
+          const uint8_t* vp = rec + a.lay.v_params + off * kP;
+          if constexpr (kP == 32) {
+            cp_async16(pat + lane * 16, kp + lane * 16);
+            cp_async16(pat + C::kParams + lane * 16, vp + lane * 16);
+          } else if (lane < 2 * kP) {
+            const int l = lane < kP ? lane : lane - kP;
+            cp_async16(pat + (lane < kP ? 0 : C::kParams) + l * 16, (lane < kP ? kp : vp) + l * 16);
+          }
         }
       }
       cp_commit();
@@ -227,7 +314,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
     }
 
     float acc[NT][HD / 16][4];
-    float m_run[NT][2], l_run[NT][2], lh_run[NT][2];
+    float m_run[NT][2], l_run[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -238,9 +325,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       for (int e = 0; e < 2; ++e) {
         m_run[n][e] = -INFINITY;
         l_run[n][e] = 0.f;
-        lh_run[n][e] = 0.f;
       }
     }
+    // V's unit: |minimum| < 2^(vexp + 14) and |scale| < 2^(vexp + 10) keep every
+    // value below 2^15; `limit` holds both bounds as a param does.
+    int vexp = 0;
+    float v_unit = 1.f;  // 2^-vexp
+    uint32_t limit = 0;
 
     // ------------------------------------------------ the walk over the tokens
 #pragma unroll 1
@@ -248,21 +339,22 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       cp_wait<C::kStages - 2>();
       __syncwarp();  // every lane's copies have landed; step i - 1 has been read
       issue(i + C::kStages - 1);
-      if (!((live >> (i & 31)) & 1u)) continue;
-      const int tok = tok0 + i * kKv4Tile;
+      const int tok = tok0 + i * kTile;
       const uint8_t* st = stage0 + (i % C::kStages) * C::kStage;
       const bool edge = tok + kStepTokens > w.blk.all_hi || tok < w.blk.all_lo;
 
-      // S^T: rows r and r + 8 are tokens t0 and t0 + 8
-      const int t0 = token_of(r);
-      float s[NT][4];
+      // S^T of both halves
+      float s[2][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-      {
-        const uint32_t* p0 = reinterpret_cast<const uint32_t*>(st + 2 * C::kCodes) + t0 * C::kGroups;
-        const uint32_t* p1 = p0 + 8 * C::kGroups;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[hf][n][e] = 0.f;
+        uint32_t p0[C::kGroups], p1[C::kGroups];
+        load_words(st + kp_at + hf * 16 * C::kParamRow, p0);
+        load_words(st + kp_at + (hf * 16 + 8) * C::kParamRow, p1);
+        const uint32_t row = static_cast<uint32_t>(k_at + hf * 16 * C::kCodeRow);
 #pragma unroll
         for (int g = 0; g < C::kGroups; ++g) {
           float d[NT][4];
@@ -273,27 +365,26 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 #pragma unroll
           for (int cc = 0; cc < GROUP / 32; ++cc) {
             const int c = g * (GROUP / 32) + cc;
-            const int at = (t0 * (HD / 32) + chunk_of<HD>(t0, c)) * 16 + q * 4;
+            const uint32_t at = row ^ static_cast<uint32_t>(c * 16);
             const uint32_t w0 = *reinterpret_cast<const uint32_t*>(st + at);
             const uint32_t w1 = *reinterpret_cast<const uint32_t*>(st + at + 8 * C::kCodeRow);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              const uint32_t af[4] = {codes2(w0, 2 * ks), codes2(w1, 2 * ks),
-                                      codes2(w0, 2 * ks + 1), codes2(w1, 2 * ks + 1)};
+              const uint32_t af[4] = {k_codes(w0, 2 * ks), k_codes(w1, 2 * ks),
+                                      k_codes(w0, 2 * ks + 1), k_codes(w1, 2 * ks + 1)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(d[n], af, qf[n][c][2 * ks], qf[n][c][2 * ks + 1]);
+              for (int n = 0; n < NT; ++n) mma_bf16(d[n], af, qf[n][c][2 * ks], qf[n][c][2 * ks + 1]);
             }
           }
-          const uint32_t k0 = p0[g], k1 = p1[g];
-          const float s0 = __uint_as_float(k0 << 16), s1 = __uint_as_float(k1 << 16);
-          const float b0 = fmaf(-128.f, s0, __uint_as_float(k0 & 0xffff0000u));
-          const float b1 = fmaf(-128.f, s1, __uint_as_float(k1 & 0xffff0000u));
+          const float s0 = param_scale(p0[g]), s1 = param_scale(p1[g]);
+          const float b0 = fmaf(-128.f, s0, param_min(p0[g]));
+          const float b1 = fmaf(-128.f, s1, param_min(p1[g]));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[n][0] = fmaf(d[n][0], s0, fmaf(b0, qsum[n][g][0], s[n][0]));
-            s[n][1] = fmaf(d[n][1], s0, fmaf(b0, qsum[n][g][1], s[n][1]));
-            s[n][2] = fmaf(d[n][2], s1, fmaf(b1, qsum[n][g][0], s[n][2]));
-            s[n][3] = fmaf(d[n][3], s1, fmaf(b1, qsum[n][g][1], s[n][3]));
+            s[hf][n][0] = fmaf(d[n][0], s0, fmaf(b0, qsum[n][g][0], s[hf][n][0]));
+            s[hf][n][1] = fmaf(d[n][1], s0, fmaf(b0, qsum[n][g][1], s[hf][n][1]));
+            s[hf][n][2] = fmaf(d[n][2], s1, fmaf(b1, qsum[n][g][0], s[hf][n][2]));
+            s[hf][n][3] = fmaf(d[n][3], s1, fmaf(b1, qsum[n][g][1], s[hf][n][3]));
           }
         }
       }
@@ -306,28 +397,81 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       };
       if (edge) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int token = tok + hf * 16 + t0 + (e & 2) * 4;
+              s[hf][n][e] = visible(token, pos[n][e & 1]) ? s[hf][n][e] : -INFINITY;
+            }
+      }
+
+      // V's params of this lane's eight tokens
+      uint32_t par[2][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          par[hf][e] = *reinterpret_cast<const uint32_t*>(
+              st + vp_at[e & 1] + (hf * 16 + (e & 2) * 4) * C::kParamRow);
+      if (edge) {
+        // Rows behind the last visible token may hold anything, and a value
+        // that is not a number must not reach rows that do not see it (see
+        // below): their weights are 0, which counts only for finite values.
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int token = tok + t0 + (e & 2) * 4;
-            s[n][e] = visible(token, pos[n][e & 1]) ? s[n][e] : -INFINITY;
+            const int token = tok + hf * 16 + ta[e & 1] + (e & 2) * 4;
+            if (token >= w.blk.hi || odd_param(par[hf][e])) par[hf][e] = 0;
           }
       }
 
-      // running maximum: moved only when some score passes it by kGrow
-      bool grow = false;
+      // Running maximum and V's unit: moved only when they are passed (by
+      // kGrow), which after the first steps of an item is rare.
+      uint32_t top_par = 0;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top_par = __vmaxu2(top_par, par[hf][e] & 0x7fff7fffu);
+      bool grow = __vmaxu2(top_par, limit) != limit;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          grow = grow || fmaxf(s[n][e], s[n][e + 2]) * a.scale_log2 > m_run[n][e] + kGrow;
+          grow = grow || fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2])) *
+                                 a.scale_log2 > m_run[n][e] + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
+        // Exponents of the largest minimum and scale of the step, numbers only.
+        int em = 0, es = 0;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!odd_param(par[hf][e])) {
+              em = max(em, static_cast<int>((par[hf][e] >> 23) & 255));
+              es = max(es, static_cast<int>((par[hf][e] >> 7) & 255));
+            }
+        em = __reduce_max_sync(0xffffffffu, em);
+        es = __reduce_max_sync(0xffffffffu, es);
+        const int want = max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
+        float shrink = 1.f;
+        if (limit == 0 || want > vexp) {
+          if (limit != 0) shrink = exp2f(static_cast<float>(max(vexp - want, -126)));
+          vexp = want;
+          v_unit = exp2f(static_cast<float>(-vexp));
+          // the largest bf16 below 2^(vexp + 14), and below 2^(vexp + 10)
+          limit = (static_cast<uint32_t>(min(vexp + 14 + 127, 255) * 128 - 1) << 16) |
+                  static_cast<uint32_t>(vexp + 10 + 127) * 128 - 1;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[n][e], s[n][e + 2]) * a.scale_log2;
+            float top = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2])) *
+                        a.scale_log2;
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -335,131 +479,100 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
             alpha[e] = up ? ex2(m_run[n][e] - top) : 1.f;
             m_run[n][e] = up ? top : m_run[n][e];
             l_run[n][e] *= alpha[e];
-            lh_run[n][e] *= alpha[e];
           }
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][k][e] *= alpha[e & 1];
+            for (int e = 0; e < 4; ++e) acc[n][k][e] *= alpha[e & 1] * shrink;
         }
       }
 
       // P^T as B fragments
-      uint32_t pf[NT][2];
+      uint32_t pf[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float m0 = m_run[n][0] == -INFINITY ? 0.f : m_run[n][0];
-        const float m1 = m_run[n][1] == -INFINITY ? 0.f : m_run[n][1];
-        const float p0 = ex2(fmaf(s[n][0], a.scale_log2, -m0));
-        const float p1 = ex2(fmaf(s[n][1], a.scale_log2, -m1));
-        const float p2 = ex2(fmaf(s[n][2], a.scale_log2, -m0));
-        const float p3 = ex2(fmaf(s[n][3], a.scale_log2, -m1));
-        const uint32_t lo = pack_bf16(p0, p1), hi = pack_bf16(p2, p3);
-        l_run[n][0] += p0 + p2;
-        l_run[n][1] += p1 + p3;
-        lh_run[n][0] += __uint_as_float(lo << 16) + __uint_as_float(hi << 16);
-        lh_run[n][1] += __uint_as_float(lo & 0xffff0000u) + __uint_as_float(hi & 0xffff0000u);
-        pf[n][0] = transpose8x8(lo);
-        pf[n][1] = transpose8x8(hi);
+        const float m0 = m_run[n][0] == -INFINITY ? 0.f : m_run[n][0] - kShift;
+        const float m1 = m_run[n][1] == -INFINITY ? 0.f : m_run[n][1] - kShift;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float p0 = ex2(fmaf(s[hf][n][0], a.scale_log2, -m0));
+          const float p1 = ex2(fmaf(s[hf][n][1], a.scale_log2, -m1));
+          const float p2 = ex2(fmaf(s[hf][n][2], a.scale_log2, -m0));
+          const float p3 = ex2(fmaf(s[hf][n][3], a.scale_log2, -m1));
+          l_run[n][0] += p0 + p2;
+          l_run[n][1] += p1 + p3;
+          pf[hf][n][0] = transpose8x8(pack_f16(p0, p1));
+          pf[hf][n][1] = transpose8x8(pack_f16(p2, p3));
+        }
       }
 
       // O^T += V^T P^T: this lane's rows are the HD / 8 channels from r HD / 8 on,
-      // its columns tokens ta, tb (first half of k) and ta + 8, tb + 8
-      {
-        const int ta0 = token_of(2 * q), ta1 = token_of(2 * q + 1);
-        const uint32_t* vp = reinterpret_cast<const uint32_t*>(st + 2 * C::kCodes + C::kParams) +
-                             (r * (HD / 8)) / GROUP;
-        uint32_t par[4] = {vp[ta0 * C::kGroups], vp[ta1 * C::kGroups], vp[(ta0 + 8) * C::kGroups],
-                           vp[(ta1 + 8) * C::kGroups]};
-        if (edge) {
-          // Rows behind the request's last token may hold anything: their
-          // weights are 0, and their values have to be finite for that to count.
+      // its columns tokens ta[0], ta[1] (first half of k) and those + 8
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int token = tok + ((e & 1) ? ta1 : ta0) + (e & 2) * 4;
-            const bool odd = (par[e] & 0x7f80u) == 0x7f80u || (par[e] & 0x7f800000u) == 0x7f800000u;
-            if (token >= w.req.kv || odd) par[e] = 0;
-          }
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t sc[2], mn[2];  // scale and minimum + 8 scale of two tokens
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float sa = param_scale(par[hf][2 * k]) * v_unit, sb = param_scale(par[hf][2 * k + 1]) * v_unit;
+          sc[k] = pack_f16(sa, sb);
+          mn[k] = pack_f16(fmaf(8.f, sa, param_min(par[hf][2 * k]) * v_unit),
+                           fmaf(8.f, sb, param_min(par[hf][2 * k + 1]) * v_unit));
         }
-        const uint32_t sc0 = __byte_perm(par[0], par[1], 0x5410), mn0 = __byte_perm(par[0], par[1], 0x7632);
-        const uint32_t sc1 = __byte_perm(par[2], par[3], 0x5410), mn1 = __byte_perm(par[2], par[3], 0x7632);
         constexpr int kWords = HD / 64;  // words of codes a lane has per token
         uint32_t v[4][kWords];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = ((e & 1) ? ta1 : ta0) + (e & 2) * 4;
-          const int byte = r * (HD / 16);
-          const uint8_t* src = st + C::kCodes +
-                               (t * (HD / 32) + chunk_of<HD>(t & 7, byte / 16)) * 16 + byte % 16;
-          if constexpr (kWords == 1) {
-            v[e][0] = *reinterpret_cast<const uint32_t*>(src);
-          } else if constexpr (kWords == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(src);
-            v[e][0] = x.x;
-            v[e][1] = x.y;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(src);
-            v[e][0] = x.x;
-            v[e][1] = x.y;
-            v[e][2] = x.z;
-            v[e][3] = x.w;
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          load_words(st + v_at[e & 1] + (hf * 16 + (e & 2) * 4) * C::kCodeRow, v[e]);
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           // Even channels of two tokens, then odd ones, in one register each.
           const uint32_t e0 = __byte_perm(v[0][j], v[1][j], 0x5410), o0 = __byte_perm(v[0][j], v[1][j], 0x7632);
           const uint32_t e1 = __byte_perm(v[2][j], v[3][j], 0x5410), o1 = __byte_perm(v[2][j], v[3][j], 0x7632);
-          constexpr uint32_t kMinus128 = 0xc300c300u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t af[4] = {fma_bf16x2(add_bf16x2(codes2(e0, k), kMinus128), sc0, mn0),
-                                    fma_bf16x2(add_bf16x2(codes2(o0, k), kMinus128), sc0, mn0),
-                                    fma_bf16x2(add_bf16x2(codes2(e1, k), kMinus128), sc1, mn1),
-                                    fma_bf16x2(add_bf16x2(codes2(o1, k), kMinus128), sc1, mn1)};
+            const uint32_t af[4] = {fma_f16x2(v_codes(e0, k), sc[0], mn[0]),
+                                    fma_f16x2(v_codes(o0, k), sc[0], mn[0]),
+                                    fma_f16x2(v_codes(e1, k), sc[1], mn[1]),
+                                    fma_f16x2(v_codes(o1, k), sc[1], mn[1])};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(acc[n][4 * j + k], af, pf[n][0], pf[n][1]);
+            for (int n = 0; n < NT; ++n) mma_f16(acc[n][4 * j + k], af, pf[hf][n][0], pf[hf][n][1]);
           }
         }
-        if (edge) {
-          // A token whose values are not numbers, seen by some rows only: those
-          // rows, and no others, take it.
+      }
+      if (edge) {
+        // A token whose values are not numbers, seen by some rows only: those
+        // rows, and no others, take it.
 #pragma unroll 1
-          for (int t = 0; t < kStepTokens; ++t) {
-            const uint32_t p = vp[t * C::kGroups];
-            const bool odd = (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
-            if (!odd || tok + t >= w.req.kv) continue;
+        for (int t = 0; t < kStepTokens; ++t) {
+          const uint32_t p = *reinterpret_cast<const uint32_t*>(
+              st + 2 * C::kCodes + C::kParams + t * C::kParamRow + (r * (HD / 8)) / GROUP * 4);
+          if (tok + t >= w.blk.hi || !odd_param(p)) continue;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (visible(tok + t, pos[n][e]))
+            for (int e = 0; e < 2; ++e)
+              if (visible(tok + t, pos[n][e]))
 #pragma unroll
-                  for (int k = 0; k < HD / 16; ++k)
-                    acc[n][k][e] = acc[n][k][e + 2] = __int_as_float(0x7fffffff);
-          }
+                for (int k = 0; k < HD / 16; ++k)
+                  acc[n][k][e] = acc[n][k][e + 2] = __int_as_float(0x7fffffff);
         }
       }
     }
     cp_wait<0>();
 
     // ------------------------------------------------ the four warps' results
-    const bool whole = ta == 0 && tb == w.blk.tiles;
-    const long long part_no = 2ll * blockIdx.x + (first_item && ta > 0 ? 0 : 1);
-    if (ta == 0 && !whole) record = kv4_split_record(w, share);
+    const bool whole = first_tile == 0 && last_tile == w.blk.tiles;
+    const long long part_no = 2ll * blockIdx.x + (first_item && first_tile > 0 ? 0 : 1);
+    if (first_tile == 0 && !whole) record = kv4_split_record(w, share);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], d);
-          lh_run[n][e] += __shfl_xor_sync(0xffffffffu, lh_run[n][e], d);
-        }
+        for (int d = 4; d < 32; d <<= 1) l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], d);
         if (r == 0) {
-          stat[0][warp][8 * n + 2 * q + e] = m_run[n][e];
+          stat[0][warp][8 * n + 2 * q + e] = m_run[n][e] - kShift;
           stat[1][warp][8 * n + 2 * q + e] = l_run[n][e];
-          stat[2][warp][8 * n + 2 * q + e] = lh_run[n][e];
         }
       }
     __syncthreads();  // and every warp's stages are free for the exchange below
@@ -476,7 +589,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
         float top = stat[0][0][row];
 #pragma unroll
         for (int v = 1; v < kWarps; ++v) top = fmaxf(top, stat[0][v][row]);
-        f[e] = m_run[n][e] == -INFINITY ? 0.f : ex2(m_run[n][e] - top);
+        f[e] = m_run[n][e] == -INFINITY ? 0.f : ex2(m_run[n][e] - kShift - top + static_cast<float>(vexp));
       }
       if (n) __syncthreads();  // the previous eight rows have been read
 #pragma unroll
@@ -507,31 +620,30 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
         float top = stat[0][0][row];
 #pragma unroll
         for (int v = 1; v < kWarps; ++v) top = fmaxf(top, stat[0][v][row]);
-        float l = 0.f, lh = 0.f;
+        float l = 0.f;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
           const float g = stat[0][v][row] == -INFINITY ? 0.f : ex2(stat[0][v][row] - top);
           l = fmaf(stat[1][v][row], g, l);
-          lh = fmaf(stat[2][v][row], g, lh);
         }
         if (whole) {
           const int gr = w.blk.row0 + row;
           const int t = gr / a.per_kv, head = w.h * a.per_kv + gr - t * a.per_kv;
           const long long o = static_cast<long long>(w.req.start + t) * a.Hq + head;
-          const float inv = lh == 0.f ? 0.f : 1.f / lh;  // a NaN sum stays one
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
           reinterpret_cast<uint2*>(a.O)[o * kQuads + c] =
               make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
           if (c == 0) a.L[o] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2f;
         } else {
           const long long o = part_no * C::kRows + row;
           reinterpret_cast<float4*>(a.part_o)[o * kQuads + c] = x;
-          if (c == 0) a.part_stat[o] = make_float4(top, l, lh, 0.f);
+          if (c == 0) a.part_stat[o] = make_float2(top, l);
         }
       }
     }
     __syncthreads();  // before the next item's copies
     first_item = false;
-    u = w.item + tb;
+    u = w.item + (a.whole_items ? 1 : last_tile);
   }
   if (tid == 0) a.split[blockIdx.x] = record;
 }
@@ -562,13 +674,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   float2 x[kVec];
 #pragma unroll
   for (int k = 0; k < kVec; ++k) x[k] = make_float2(0.f, 0.f);
-  float l = 0.f, lh = 0.f;
+  float l = 0.f;
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const float4 st = a.part_stat[place(p)];
-    const float f = st.x == -INFINITY ? (st.y == st.y ? 0.f : st.y) : ex2(st.x - top);
+    const float2 st = a.part_stat[place(p)];
+    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
     l = fmaf(st.y, f, l);
-    lh = fmaf(st.z, f, lh);
     const float2* src = reinterpret_cast<const float2*>(a.part_o + place(p) * HD);
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
@@ -580,7 +691,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int gr = rec.y + row;
   const int t = gr / a.per_kv, head = h * a.per_kv + gr - t * a.per_kv;
   const long long o = static_cast<long long>(rec.x + t) * a.Hq + head;
-  const float inv = lh == 0.f ? 0.f : 1.f / lh;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.O) + o * (HD / 2);
 #pragma unroll
   for (int k = 0; k < kVec; ++k) dst[lane + 32 * k] = pack_bf16(x[k].x * inv, x[k].y * inv);
@@ -625,7 +736,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   const int ctas = per_sm * sms < kKv4MaxCtas ? per_sm * sms : kKv4MaxCtas;
   kv4_attn_kernel<HD, GROUP, NT><<<ctas, kAttnThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole_items) return e;
   return launch_merge<HD>(a, ctas, C::kRows, stream);
 }
 
@@ -654,7 +765,7 @@ int kv4_attn_rows(int d, int rows) {
 
 size_t kv4_attn_workspace(int d, int rows) {
   const size_t parts = 2 * static_cast<size_t>(kKv4MaxCtas) * kv4_attn_rows(d, rows);
-  return align256(kKv4MaxCtas * sizeof(int4)) + align256(parts * sizeof(float4)) +
+  return align256(kKv4MaxCtas * sizeof(int4)) + align256(parts * sizeof(float2)) +
          align256(parts * d * sizeof(float));
 }
 
@@ -663,9 +774,12 @@ cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cu
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.split = reinterpret_cast<int4*>(ws);
   ws += align256(kKv4MaxCtas * sizeof(int4));
-  a.part_stat = reinterpret_cast<float4*>(ws);
-  ws += align256(parts * sizeof(float4));
+  a.part_stat = reinterpret_cast<float2*>(ws);
+  ws += align256(parts * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(ws);
+  // With at most four tiles to an item, cutting it saves less than the merge
+  // costs (one more launch).
+  a.whole_items = (static_cast<long long>(a.max_pages) << a.lay.page_shift) <= 4 * kTile;
   const bool g32 = group == 32;
   switch (d) {
     case 64: return g32 ? launch_attn_rows<64, 32>(a, stream) : launch_attn_rows<64, 64>(a, stream);

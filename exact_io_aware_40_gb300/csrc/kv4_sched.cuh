@@ -4,17 +4,17 @@
 // h.  A request's rows are its n queries times the per_kv query heads that
 // share a K/V head (row = query * per_kv + head in the group), so that a tile of
 // the cache that was read once serves all of them.  An item is a run of
-// 64-token tiles, those that hold a key visible to one of its rows (at least
+// kTile-token tiles, those that hold a key visible to one of its rows (at least
 // one, so that a block that sees nothing still writes its zeros).  All tiles of
 // all items form one list which is cut into equal shares, one per CTA: lengths
 // may differ by any factor and the shares do not.  An item that a share's end
-// cuts is finished from partial results (kv4_merge.cu).
+// cuts is finished from partial results by a second kernel.  Where no item is
+// long (whole_items) a place in the list is an item instead, and that kernel is
+// not needed.
 #pragma once
 #include "kv4.h"
 
 namespace fa {
-
-constexpr int kKv4Tile = 64;
 
 struct Kv4Req {
   int start, n, kv;  // first row of Q, queries, keys
@@ -40,8 +40,10 @@ struct Kv4Block {
   int lo, hi;             // keys that some row sees
   int all_lo, all_hi;     // keys that every row sees
   int tile_lo, tiles;
+  int units;              // places in the list: tiles, or 1 if items are not cut
 };
 
+template <int kTile>
 __device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req& r, int rb,
                                               int block_rows) {
   Kv4Block k;
@@ -62,17 +64,19 @@ __device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req
     k.lo = max(k.pos0 + first - min(a.window, 0x3fffffff), 0);
     k.all_lo = max(k.pos0 + last - min(a.window, 0x3fffffff), 0);
   }
-  k.tile_lo = k.lo / kKv4Tile;
-  k.tiles = max((k.hi + kKv4Tile - 1) / kKv4Tile - k.tile_lo, 1);
+  k.tile_lo = k.lo / kTile;
+  k.tiles = max((k.hi + kTile - 1) / kTile - k.tile_lo, 1);
+  k.units = a.whole_items ? 1 : k.tiles;
   return k;
 }
 
+template <int kTile>
 __device__ __forceinline__ long long kv4_units(const Kv4AttnArgs& a, int b, int block_rows,
                                                bool* bad) {
   const Kv4Req r = kv4_request(a, b, bad);
   const int blocks = (r.n * a.per_kv + block_rows - 1) / block_rows;
   long long n = 0;
-  for (int rb = 0; rb < blocks; ++rb) n += kv4_block(a, r, rb, block_rows).tiles;
+  for (int rb = 0; rb < blocks; ++rb) n += kv4_block<kTile>(a, r, rb, block_rows).units;
   return n * a.Hkv;
 }
 
@@ -85,14 +89,14 @@ struct Kv4Share {
 // The whole block finds its share; `scratch` holds kThreads / 32 + 2 long longs.
 // Shares are at least min_tiles long.  begin/b are set when the share is not
 // empty (blockIdx.x * per < total).
-template <int kThreads>
+template <int kTile, int kThreads>
 __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_rows, int min_tiles,
                                               long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
-  long long first = tid < a.B ? kv4_units(a, tid, block_rows, &bad) : 0;
+  long long first = tid < a.B ? kv4_units<kTile>(a, tid, block_rows, &bad) : 0;
   long long sum = first;
-  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += kv4_units(a, b, block_rows, &bad);
+  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += kv4_units<kTile>(a, b, block_rows, &bad);
   if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -111,7 +115,7 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
   for (int base = 0; base < a.B; base += kThreads) {
     const int b = base + tid;
     long long v = first;
-    if (base) v = b < a.B ? kv4_units(a, b, block_rows, &bad) : 0;
+    if (base) v = b < a.B ? kv4_units<kTile>(a, b, block_rows, &bad) : 0;
     long long incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -137,6 +141,7 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
 }
 
 // A CTA's walk through its share, item by item.
+template <int kTile>
 struct Kv4Walk {
   Kv4Req req;
   Kv4Block blk;
@@ -149,7 +154,7 @@ struct Kv4Walk {
     blocks = (req.n * a.per_kv + block_rows - 1) / block_rows;
     rb = 0;
     h = 0;
-    if (blocks) blk = kv4_block(a, req, 0, block_rows);
+    if (blocks) blk = kv4_block<kTile>(a, req, 0, block_rows);
   }
   // To the item that holds tile u of the list, from the request that holds it.
   __device__ __forceinline__ void seek(const Kv4AttnArgs& a, const Kv4Share& s, long long u,
@@ -157,20 +162,20 @@ struct Kv4Walk {
     b = s.b;
     item = s.begin;
     open(a, block_rows);
-    while (u >= item + static_cast<long long>(blk.tiles) * a.Hkv) {
-      item += static_cast<long long>(blk.tiles) * a.Hkv;
+    while (u >= item + static_cast<long long>(blk.units) * a.Hkv) {
+      item += static_cast<long long>(blk.units) * a.Hkv;
       ++rb;
-      blk = kv4_block(a, req, rb, block_rows);
+      blk = kv4_block<kTile>(a, req, rb, block_rows);
     }
-    h = static_cast<int>((u - item) / blk.tiles);
-    item += static_cast<long long>(h) * blk.tiles;
+    h = static_cast<int>((u - item) / blk.units);
+    item += static_cast<long long>(h) * blk.units;
   }
   __device__ __forceinline__ void next(const Kv4AttnArgs& a, int block_rows) {
-    item += blk.tiles;
+    item += blk.units;
     if (++h < a.Hkv) return;
     h = 0;
     if (++rb < blocks) {
-      blk = kv4_block(a, req, rb, block_rows);
+      blk = kv4_block<kTile>(a, req, rb, block_rows);
       return;
     }
     while (++b < a.B) {
@@ -185,9 +190,10 @@ struct Kv4Walk {
 // z: rows + 256 * K/V head, 0: there is none, w: the last CTA with a part of
 // it).  Partial results of CTA i are number 2 i (of its first item, begun
 // before) and 2 i + 1 (of its last, begun here).
-__device__ __forceinline__ int4 kv4_split_record(const Kv4Walk& w, const Kv4Share& s) {
+template <int kTile>
+__device__ __forceinline__ int4 kv4_split_record(const Kv4Walk<kTile>& w, const Kv4Share& s) {
   return make_int4(w.req.start, w.blk.row0, w.blk.rows + 256 * w.h,
-                   static_cast<int>((w.item + w.blk.tiles - 1) / s.per));
+                   static_cast<int>((w.item + w.blk.units - 1) / s.per));
 }
 
 }  // namespace fa

@@ -340,13 +340,22 @@ def attention_bwd(q, k, v, o, do, L, causal=False, scale=None, kv_len=None, work
 
 
 # ------------------------------------------------------------------ paged 4-bit cache
+#
+# A decode step's kernels take a few microseconds, so these calls check their
+# arguments with few attribute reads and hand ctypes plain integers.
+
+_KV4_RECORD = {}  # (d, page_size, group) -> bytes of a page of one head
+
 
 def kv4_page_bytes(d, page_size, group=32):
     """Bytes of one page of one K/V head; raises for an unsupported geometry."""
-    n = int(load_library().fa_kv4_page_bytes(d, page_size, group))
-    if n == 0:
-        raise ValueError("d must be 64, 128 or 256, page_size 16, 32, 64 or 128 and group 32 or "
-                         "64, got %s, %s, %s" % (d, page_size, group))
+    n = _KV4_RECORD.get((d, page_size, group))
+    if n is None:
+        n = int(load_library().fa_kv4_page_bytes(d, page_size, group))
+        if n == 0:
+            raise ValueError("d must be 64, 128 or 256, page_size 16, 32, 64 or 128 and group 32 "
+                             "or 64, got %s, %s, %s" % (d, page_size, group))
+        _KV4_RECORD[d, page_size, group] = n
     return n
 
 
@@ -358,45 +367,52 @@ def kv4_cache(num_pages, kv_heads, page_size, d, group=32, device="cuda"):
                        device=device)
 
 
-def _expect_cache(cache, page_size, d, group):
-    """Checks a cache tensor against its geometry; returns (num_pages, kv_heads)."""
-    import torch
-    record = kv4_page_bytes(d, page_size, group)
-    if cache.dim() != 3:
-        raise ValueError("expected a [num_pages, kv_heads, page bytes] cache")
-    pages, heads = cache.shape[0], cache.shape[1]
-    _expect(cache, "cache", torch.uint8, (pages, heads, record))
-    return pages, heads
+def _need(t, name, dtype, shape, dev):
+    """Checks a contiguous tensor on CUDA device number `dev`."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _expect(t, name, dtype, tuple(shape))
+        raise ValueError("all tensors must be on one CUDA device, got %s on cuda:%d and %s on cuda:%d"
+                         % (name, t.get_device(), "others", dev))
 
 
-def _expect_rows(t, name, shape):
-    """Checks a bf16 [tokens, heads, d] CUDA tensor; returns its token and head strides."""
+def _need_rows(t, name, shape, dev):
+    """Checks a bf16 [tokens, heads, d] tensor of any strides the kernels take; returns its
+    token and head strides."""
     import torch
-    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != shape or t.stride(2) != 1:
-        raise ValueError("%s must be a CUDA torch.bfloat16 tensor of shape %s with contiguous "
-                         "channels" % (name, shape))
-    ts, hs = (st if n > 1 else 0 for st, n in zip(t.stride()[:2], shape))
+    ts, hs, cs = t.stride()
+    if t.dtype != torch.bfloat16 or t.shape != shape or cs != 1 or t.get_device() != dev:
+        raise ValueError("%s must be a torch.bfloat16 tensor of shape %s with contiguous channels "
+                         "on the CUDA device of the others" % (name, tuple(shape)))
+    ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
     if ts % 8 or hs % 8 or max(ts, hs) > 0x7fffffff or t.data_ptr() % 16:
         raise ValueError("%s: strides must be multiples of 8 elements (below 2^31) and the data "
                          "16-byte aligned" % name)
     return ts, hs
 
 
-def _expect_i32(t, name, shape):
+def _need_cache(cache, page_size, d, group):
+    """Checks a cache tensor against its geometry; returns (num_pages, kv_heads, device)."""
     import torch
-    _expect(t, name, torch.int32, shape)
+    if cache.dim() != 3:
+        raise ValueError("expected a [num_pages, kv_heads, page bytes] cache")
+    pages, heads, record = cache.shape
+    if (record != kv4_page_bytes(d, page_size, group) or cache.dtype != torch.uint8
+            or not cache.is_cuda or not cache.is_contiguous()):
+        _expect(cache, "cache", torch.uint8, (pages, heads, kv4_page_bytes(d, page_size, group)))
+    return pages, heads, cache.get_device()
 
 
-def _on_device(device, stream):
-    """Makes `device`, and `stream` if one is given, current for a call: what the call
-    allocates then belongs to the stream that uses it."""
-    import contextlib
+def _enqueue(dev, stream, call):
+    """call(raw stream) with device `dev` current, and `stream` (a raw stream) if one is given:
+    what the call allocates then belongs to the stream that uses it."""
     import torch
     if stream is not None:
-        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
+            return call(int(stream))
+    if torch.cuda.current_device() == dev:
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def kv4_plan(past_len, new_len, block_table, free_list, free_state, page_size, max_tokens,
@@ -406,82 +422,83 @@ def kv4_plan(past_len, new_len, block_table, free_list, free_state, page_size, m
     past_len, new_len: CUDA int32 [B] (new_len -1: the request is finished); block_table int32
     [B, max_pages] and free_list int32 [num_pages] are updated in place; free_state int32 [>= 2]
     (first free entry, number): the state an earlier call returned.  Returns (kv_len [B],
-    cu_q [B + 1], slots [max_tokens], state [4])."""
+    cu_q [B + 1], slots [max_tokens], state [4]), views of one buffer."""
     import torch
-    B = past_len.numel()
     if block_table.dim() != 2:
         raise ValueError("expected a [B, max_pages] block_table")
-    max_pages = block_table.shape[1]
-    num_pages = free_list.numel() if num_pages is None else int(num_pages)
-    _expect_i32(past_len, "past_len", (B,))
-    _expect_i32(new_len, "new_len", (B,))
-    _expect_i32(block_table, "block_table", (B, max_pages))
-    _expect_i32(free_list, "free_list", (num_pages,))
-    _expect_i32(free_state, "free_state", (free_state.numel(),))
-    if free_state.numel() < 2:
-        raise ValueError("free_state must hold the first free entry and their number")
-    if max_tokens < 1:
-        raise ValueError("max_tokens must be positive")
-    _same_device(past_len, new_len, block_table, free_list, free_state)
-    dev = past_len.device
-    # one allocation; each part starts on a 16-byte boundary
-    r4 = lambda n: (n + 3) // 4 * 4
-    n_kv, n_cu, n_slots = r4(B), r4(B + 1), r4(max_tokens)
-    with _on_device(dev, stream):
-        out = torch.empty(n_kv + n_cu + n_slots + 4, dtype=torch.int32, device=dev)
-        kv_len, cu_q = out[:B], out[n_kv:n_kv + B + 1]
-        slots = out[n_kv + n_cu:n_kv + n_cu + max_tokens]
-        state = out[n_kv + n_cu + n_slots:]
+    B, max_pages = block_table.shape
+    n = free_list.numel()
+    if num_pages is not None and num_pages != n:
+        raise ValueError("free_list must hold num_pages entries")
+    dev, i32 = past_len.get_device(), torch.int32
+    _need(past_len, "past_len", i32, (B,), dev)
+    _need(new_len, "new_len", i32, (B,), dev)
+    _need(block_table, "block_table", i32, (B, max_pages), dev)
+    _need(free_list, "free_list", i32, (n,), dev)
+    state_n = free_state.numel()
+    _need(free_state, "free_state", i32, (state_n,), dev)
+    if dev < 0:
+        raise ValueError("past_len must be a CUDA tensor")
+    if state_n < 2 or max_tokens < 1:
+        raise ValueError("free_state must hold the first free entry and their number, and "
+                         "max_tokens be positive")
+
+    def call(raw):
+        out = torch.empty(2 * B + 5 + max_tokens, dtype=i32, device=past_len.device)
+        at = out.data_ptr()
         _check(load_library().fa_kv4_plan(
-            _ptr(past_len), _ptr(new_len), B, page_size, num_pages, _ptr(block_table), max_pages,
-            _ptr(free_list), _ptr(free_state), max_tokens, _ptr(kv_len), _ptr(cu_q), _ptr(slots),
-            _ptr(state), _stream(stream, past_len)), "fa_kv4_plan")
-    return kv_len, cu_q, slots, state
+            past_len.data_ptr(), new_len.data_ptr(), B, page_size, n, block_table.data_ptr(),
+            max_pages, free_list.data_ptr(), free_state.data_ptr(), max_tokens, at, at + 4 * B,
+            at + 4 * (2 * B + 1), at + 4 * (2 * B + 1 + max_tokens), raw), "fa_kv4_plan")
+        return out
+
+    return _enqueue(dev, stream, call).split_with_sizes((B, B + 1, max_tokens, 4))
 
 
 def kv4_append(k, v, slots, cache, page_size, group=32, stream=None):
     """Quantises k, v (bf16 [T, kv_heads, d], views of a packed projection allowed) and writes
     them to their slots (CUDA int32 [T], -1 skips) in the cache (fa_kv4_append)."""
-    if k.dim() != 3:
+    import torch
+    if k.dim() != 3 or v.dim() != 3:
         raise ValueError("expected [T, kv_heads, d] keys and values")
-    T, heads, d = (int(x) for x in k.shape)
-    pages, cache_heads = _expect_cache(cache, page_size, d, group)
+    shape = k.shape
+    T, heads, d = shape
+    pages, cache_heads, dev = _need_cache(cache, page_size, d, group)
     if heads != cache_heads:
         raise ValueError("k has %d heads, the cache %d" % (heads, cache_heads))
-    k_ts, k_hs = _expect_rows(k, "k", (T, heads, d))
-    v_ts, v_hs = _expect_rows(v, "v", (T, heads, d))
-    _expect_i32(slots, "slots", (T,))
-    _same_device(k, v, slots, cache)
+    k_ts, k_hs = _need_rows(k, "k", shape, dev)
+    v_ts, v_hs = _need_rows(v, "v", shape, dev)
+    _need(slots, "slots", torch.int32, (T,), dev)
     if T == 0:
         return
-    with _on_device(cache.device, stream):
-        _check(load_library().fa_kv4_append(
-            _ptr(k), _ptr(v), T, heads, d, k_ts, k_hs, v_ts, v_hs,
-            _ptr(slots), _ptr(cache), pages, page_size, group, _stream(stream, cache)),
-            "fa_kv4_append")
+    _enqueue(dev, stream, lambda raw: _check(load_library().fa_kv4_append(
+        k.data_ptr(), v.data_ptr(), T, heads, d, k_ts, k_hs, v_ts, v_hs, slots.data_ptr(),
+        cache.data_ptr(), pages, page_size, group, raw), "fa_kv4_append"))
 
 
 def kv4_gather(slots, cache, page_size, d, group=32, out_k=None, out_v=None, stream=None):
     """The values the cache holds at `slots` (CUDA int32 [T]): bf16 (K, V), each
     [T, kv_heads, d].  Rows whose slot is -1 are not written (fa_kv4_gather)."""
     import torch
-    pages, heads = _expect_cache(cache, page_size, d, group)
+    pages, heads, dev = _need_cache(cache, page_size, d, group)
     T = slots.numel()
-    _expect_i32(slots, "slots", (T,))
-    shape = (T, heads, d)
-    _same_device(slots, cache, out_k, out_v)
-    with _on_device(cache.device, stream):
-        if out_k is None:
-            out_k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        if out_v is None:
-            out_v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        _expect(out_k, "out_k", torch.bfloat16, shape)
-        _expect(out_v, "out_v", torch.bfloat16, shape)
+    bf16, shape = torch.bfloat16, (T, heads, d)
+    _need(slots, "slots", torch.int32, (T,), dev)
+    if out_k is not None:
+        _need(out_k, "out_k", bf16, shape, dev)
+    if out_v is not None:
+        _need(out_v, "out_v", bf16, shape, dev)
+
+    def call(raw):
+        K = torch.empty(shape, dtype=bf16, device=cache.device) if out_k is None else out_k
+        V = torch.empty(shape, dtype=bf16, device=cache.device) if out_v is None else out_v
         if T:
             _check(load_library().fa_kv4_gather(
-                _ptr(slots), _ptr(cache), pages, page_size, group, T, heads, d, _ptr(out_k),
-                _ptr(out_v), _stream(stream, cache)), "fa_kv4_gather")
-    return out_k, out_v
+                slots.data_ptr(), cache.data_ptr(), pages, page_size, group, T, heads, d,
+                K.data_ptr(), V.data_ptr(), raw), "fa_kv4_gather")
+        return K, V
+
+    return _enqueue(dev, stream, call)
 
 
 def kv4_attention_workspace_bytes(q_heads, kv_heads, d, max_q):
@@ -497,45 +514,50 @@ def kv4_attention(q, cache, block_table, cu_q, kv_len, max_q, page_size, group=3
     has rows cu_q[b] .. cu_q[b + 1] - 1, at most max_q of them, its last tokens); kv_len int32
     [B], new tokens included.  Query heads h * q_heads / kv_heads .. share K/V head h.  Returns
     (O bf16 [total_q, q_heads, d], L fp32 [total_q, q_heads]); rows behind the last request are
-    not written."""
+    not written.  A workspace (uint8, kv4_attention_workspace_bytes) must not be shared by
+    calls that may overlap."""
     import torch
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("expected [total_q, q_heads, d] queries and a [B, max_pages] block_table")
-    total, q_heads, d = (int(x) for x in q.shape)
-    pages, kv_heads = _expect_cache(cache, page_size, d, group)
-    B, max_pages = (int(x) for x in block_table.shape)
-    q_ts, q_hs = _expect_rows(q, "q", (total, q_heads, d))
+    shape = q.shape
+    total, q_heads, d = shape
+    pages, kv_heads, dev = _need_cache(cache, page_size, d, group)
+    B, max_pages = block_table.shape
+    i32 = torch.int32
+    q_ts, q_hs = _need_rows(q, "q", shape, dev)
     if q_heads % kv_heads:
         raise ValueError("%d query heads do not divide into %d K/V heads" % (q_heads, kv_heads))
-    _expect_i32(block_table, "block_table", (B, max_pages))
-    _expect_i32(cu_q, "cu_q", (B + 1,))
-    _expect_i32(kv_len, "kv_len", (B,))
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    if max_q < 1:
+        raise ValueError("max_q must be positive")
+    _need(block_table, "block_table", i32, (B, max_pages), dev)
+    _need(cu_q, "cu_q", i32, (B + 1,), dev)
+    _need(kv_len, "kv_len", i32, (B,), dev)
     if out is not None:
-        _expect(out, "out", torch.bfloat16, (total, q_heads, d))
+        _need(out, "out", torch.bfloat16, shape, dev)
     if lse is not None:
-        _expect(lse, "lse", torch.float32, (total, q_heads))
+        _need(lse, "lse", torch.float32, (total, q_heads), dev)
     if workspace is not None:
-        _expect(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    _same_device(q, cache, block_table, cu_q, kv_len, out, lse, workspace)
-    dev = q.device
-    with _on_device(dev, stream):
-        if out is None:
-            out = torch.empty((total, q_heads, d), dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty((total, q_heads), dtype=torch.float32, device=dev)
-        if total == 0 or B == 0:
-            return out, lse
-        if workspace is None:
-            workspace = torch.empty(kv4_attention_workspace_bytes(q_heads, kv_heads, d, max_q),
-                                    dtype=torch.uint8, device=dev)
-        _check(load_library().fa_kv4_attn(
-            _ptr(q), _ptr(cache), _ptr(block_table), _ptr(cu_q), _ptr(kv_len), _ptr(out),
-            _ptr(lse), B, total, max_q, q_heads, kv_heads, d, q_ts, q_hs, pages, max_pages,
-            page_size, group, float(scale), int(bool(causal)), int(window), _ptr(workspace),
-            workspace.numel(), _stream(stream, q)), "fa_kv4_attn")
-    return out, lse
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+
+    def call(raw):
+        at = q.device
+        O = torch.empty(shape, dtype=torch.bfloat16, device=at) if out is None else out
+        L = torch.empty((total, q_heads), dtype=torch.float32, device=at) if lse is None else lse
+        if total and B:
+            lib = load_library()
+            ws = workspace
+            if ws is None:
+                ws = torch.empty(lib.fa_kv4_attn_workspace_bytes(q_heads, kv_heads, d, max_q),
+                                 dtype=torch.uint8, device=at)
+            _check(lib.fa_kv4_attn(
+                q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                kv_len.data_ptr(), O.data_ptr(), L.data_ptr(), B, total, max_q, q_heads, kv_heads, d,
+                q_ts, q_hs, pages, max_pages, page_size, group,
+                1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, window,
+                ws.data_ptr(), ws.numel(), raw), "fa_kv4_attn")
+        return O, L
+
+    return _enqueue(dev, stream, call)
 
 
 # ------------------------------------------------------------------ autograd

@@ -27,8 +27,9 @@
  *
  * Errors inside the data (a slot or a page id outside the cache, offsets in
  * cu_q that do not fit, an inconsistent free list) cannot be returned by a call
- * that only enqueues: the kernels skip what is out of range, touch no memory
- * outside the buffers, and fa_check_error() returns FA_ERR_INVALID_ARG.
+ * that only enqueues: the kernels touch no memory outside the buffers, skip the
+ * row or the request concerned (a page id out of range gives that request an
+ * undefined result), and fa_check_error() returns FA_ERR_INVALID_ARG.
  */
 #ifndef FA_KV4_H_
 #define FA_KV4_H_
