@@ -87,12 +87,17 @@ struct Kv4AttnArgs {
   float* part_o;
 };
 
-// CTAs of a launch never exceed this, so that the workspace's size does not
+// CTAs of a launch never exceed these, so that the workspace's size does not
 // depend on the device.
-constexpr int kKv4MaxCtas = 640;
-// Query rows (queries x heads per K/V head) of one CTA's block.
+constexpr int kKv4MaxCtas = 640;       // few query rows (kv4_attn.cu)
+constexpr int kKv4MaxChunkCtas = 320;  // many (kv4_chunk.cu)
+constexpr int kKv4ChunkRows = 128;
+// Query rows of one CTA's block, given the most rows (queries x heads per K/V
+// head) a request may have; kKv4ChunkRows selects the kernel for many.
 int kv4_attn_rows(int d, int rows);
 size_t kv4_attn_workspace(int d, int rows);
 cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cudaStream_t stream);
+// The kernel for many rows; *ctas: CTAs launched, for the merge that follows.
+cudaError_t launch_kv4_chunk(int d, int group, const Kv4AttnArgs& a, cudaStream_t stream, int* ctas);
 
 }  // namespace fa

@@ -66,6 +66,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b: a zero accumulator that takes no registers
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -347,10 +356,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       float s[2][NT][4];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[hf][n][e] = 0.f;
         uint32_t p0[C::kGroups], p1[C::kGroups];
         load_words(st + kp_at + hf * 16 * C::kParamRow, p0);
         load_words(st + kp_at + (hf * 16 + 8) * C::kParamRow, p1);
@@ -358,10 +363,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 #pragma unroll
         for (int g = 0; g < C::kGroups; ++g) {
           float d[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll
           for (int cc = 0; cc < GROUP / 32; ++cc) {
             const int c = g * (GROUP / 32) + cc;
@@ -373,7 +374,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
               const uint32_t af[4] = {k_codes(w0, 2 * ks), k_codes(w1, 2 * ks),
                                       k_codes(w0, 2 * ks + 1), k_codes(w1, 2 * ks + 1)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_bf16(d[n], af, qf[n][c][2 * ks], qf[n][c][2 * ks + 1]);
+              for (int n = 0; n < NT; ++n) {
+                if (cc == 0 && ks == 0)
+                  mma_bf16_first(d[n], af, qf[n][c][0], qf[n][c][1]);
+                else
+                  mma_bf16(d[n], af, qf[n][c][2 * ks], qf[n][c][2 * ks + 1]);
+              }
             }
           }
           const float s0 = param_scale(p0[g]), s1 = param_scale(p1[g]);
@@ -381,10 +387,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
           const float b1 = fmaf(-128.f, s1, param_min(p1[g]));
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[hf][n][0] = fmaf(d[n][0], s0, fmaf(b0, qsum[n][g][0], s[hf][n][0]));
-            s[hf][n][1] = fmaf(d[n][1], s0, fmaf(b0, qsum[n][g][1], s[hf][n][1]));
-            s[hf][n][2] = fmaf(d[n][2], s1, fmaf(b1, qsum[n][g][0], s[hf][n][2]));
-            s[hf][n][3] = fmaf(d[n][3], s1, fmaf(b1, qsum[n][g][1], s[hf][n][3]));
+            float* z = s[hf][n];
+            const float q0 = qsum[n][g][0], q1 = qsum[n][g][1];
+            z[0] = fmaf(d[n][0], s0, g ? fmaf(b0, q0, z[0]) : b0 * q0);
+            z[1] = fmaf(d[n][1], s0, g ? fmaf(b0, q1, z[1]) : b0 * q1);
+            z[2] = fmaf(d[n][2], s1, g ? fmaf(b1, q0, z[2]) : b1 * q0);
+            z[3] = fmaf(d[n][3], s1, g ? fmaf(b1, q1, z[3]) : b1 * q1);
           }
         }
       }
@@ -743,6 +751,11 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
 template <int HD, int GROUP>
 cudaError_t launch_attn_rows(const Kv4AttnArgs& a, cudaStream_t stream) {
   switch (kv4_attn_rows(HD, a.max_q * a.per_kv)) {
+    case kKv4ChunkRows: {
+      int ctas = 0;
+      const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
+      return e != cudaSuccess ? e : launch_merge<HD>(a, ctas, kKv4ChunkRows, stream);
+    }
     case 8: return launch_attn<HD, GROUP, 1>(a, stream);
     case 16: return launch_attn<HD, GROUP, 2>(a, stream);
     default:
@@ -759,18 +772,26 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 int kv4_attn_rows(int d, int rows) {
   if (rows <= 8) return 8;
-  if (rows <= 16 || d == 256) return 16;  // d = 256: 32 rows of O would not fit the registers
-  return 32;
+  if (rows <= 16) return 16;
+  if (rows <= 32 && d != 256) return 32;  // d = 256: 32 rows of O would not fit the registers
+  return kKv4ChunkRows;
 }
 
+namespace {
+size_t part_rows(int d, int rows) {  // rows of all partial results
+  const int block = kv4_attn_rows(d, rows);
+  return 2 * static_cast<size_t>(block == kKv4ChunkRows ? kKv4MaxChunkCtas : kKv4MaxCtas) * block;
+}
+}  // namespace
+
 size_t kv4_attn_workspace(int d, int rows) {
-  const size_t parts = 2 * static_cast<size_t>(kKv4MaxCtas) * kv4_attn_rows(d, rows);
+  const size_t parts = part_rows(d, rows);
   return align256(kKv4MaxCtas * sizeof(int4)) + align256(parts * sizeof(float2)) +
          align256(parts * d * sizeof(float));
 }
 
 cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cudaStream_t stream) {
-  const size_t parts = 2 * static_cast<size_t>(kKv4MaxCtas) * kv4_attn_rows(d, a.max_q * a.per_kv);
+  const size_t parts = part_rows(d, a.max_q * a.per_kv);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.split = reinterpret_cast<int4*>(ws);
   ws += align256(kKv4MaxCtas * sizeof(int4));
@@ -779,7 +800,8 @@ cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cu
   a.part_o = reinterpret_cast<float*>(ws);
   // With at most four tiles to an item, cutting it saves less than the merge
   // costs (one more launch).
-  a.whole_items = (static_cast<long long>(a.max_pages) << a.lay.page_shift) <= 4 * kTile;
+  a.whole_items = kv4_attn_rows(d, a.max_q * a.per_kv) != kKv4ChunkRows &&
+                  (static_cast<long long>(a.max_pages) << a.lay.page_shift) <= 4 * kTile;
   const bool g32 = group == 32;
   switch (d) {
     case 64: return g32 ? launch_attn_rows<64, 32>(a, stream) : launch_attn_rows<64, 64>(a, stream);

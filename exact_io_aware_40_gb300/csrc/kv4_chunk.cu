@@ -1,0 +1,783 @@
+// kv4_chunk.cu -- attention over the paged 4-bit cache for many query rows: a
+// chunk of a prompt, or drafted tokens of many query heads.
+//
+// One CTA takes blocks of 128 query rows (queries x query heads of one K/V head)
+// and walks its share of the tiles of 64 tokens (kv4_sched.cuh).  Both products
+// run on the tensor cores out of tensor memory as in the bf16 forward (S double
+// buffered, P over S as the A operand of P V, O resident); what differs is where
+// K and V come from:
+//   - warps 4-7 read a tile's codes and params (16 bytes a thread, a row's
+//     threads side by side) one tile ahead into registers and write them as fp16
+//     tiles in the 128-byte-swizzled layout the products take;
+//   - warps 0-3 (thread = row = TMEM lane) load Q, do the softmax and write O;
+//   - one thread of warp 8 issues the products.
+//
+// K.  (code - 8) * scale has at most 8 + 3 significant bits and so is exact in
+// fp16, as Q is (8 bits) after a scaling of each row by a power of two.  The
+// rest of a key, minimum + 8 scale of each group, meets the sum of Q over the
+// group; both are split into two fp16 (22 bits) and their three leading products
+// are slots of one more k-step (two if there are eight groups).  So scores have
+// the accuracy of fp32 sums without a second pass over K.
+// V.  minimum + scale * code rounded to fp16, P in fp16: see kv4_attn.cu.
+// fp16's range: the K and V of a tile are taken in units of a power of two that
+// fits the tile's largest param.  K's unit multiplies the tile's scores; V's goes
+// into the exponent of P, whose reference then includes the largest unit so far.
+//
+// Bound: the tensor cores (4 d FLOP a score) and, near it, the instructions of
+// the two warpgroups: a tile costs about 15 for eight codes and 3.5 for a score
+// against 616 clocks of products at d = 128.  Two CTAs per SM (d <= 128) cover
+// each other's waits.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "kernels.h"
+#include "kv4.h"
+#include "kv4_sched.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTile = 64;
+constexpr int kThreads = 288;
+constexpr float kGrow = 4.f;
+constexpr float kShift = 10.f;
+constexpr float kLn2f = 0.693147180559945309f;
+constexpr int kUnits = 4;  // ring of tile units: a tile's is read before tile + 4 is converted
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t keep, uint32_t set) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(keep), "r"(set));
+  return r;
+}
+// Channels 2 i and 2 i + 1 of a word as fp16 values code - 8.
+__device__ __forceinline__ uint32_t codes_m8(uint32_t w, int i) {
+  const uint32_t x = i < 2 ? w : w >> 8;
+  if ((i & 1) == 0) return add_f16x2(and_or(x, 0x000f000fu, 0x64006400u), 0xe408e408u);  // -1032
+  return fma_f16x2(and_or(x, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+}
+__device__ __forceinline__ bool odd_param(uint32_t p) {
+  return (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float param_min(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Instruction descriptor of kind::f16 with fp16 A and B (format 0), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// Shared-memory descriptor without swizzle, K-major: core matrices of 8 rows x
+// 16 bytes, `lbo` bytes apart along K and `sbo` bytes apart along the rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+
+template <int HD, int GROUP>
+struct Cfg {
+  static constexpr int kGroups = HD / GROUP;
+  static constexpr int kAtoms = HD / 64;
+  static constexpr int kQAtom = kRows * 128, kQTile = kAtoms * kQAtom;
+  static constexpr int kAtom = kTile * 128, kTileBytes = kAtoms * kAtom;  // K or V tile
+  // Extra slots: three for each group, in k-steps of 16.
+  static constexpr int kExSteps = (3 * kGroups + 15) / 16;
+  static constexpr int kExRow8 = kExSteps * 256;  // bytes of eight rows
+  static constexpr int kQEx = kRows / 8 * kExRow8, kKEx = kTile / 8 * kExRow8;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kQTile;
+  static constexpr int kOffV = kOffK + 2 * kTileBytes;
+  static constexpr int kOffQEx = kOffV + 2 * kTileBytes;
+  static constexpr int kOffKEx = kOffQEx + kQEx;
+  static constexpr int kOffBar = kOffKEx + 2 * kKEx;
+  // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, drain
+  static constexpr int kNumBar = 15;
+  static constexpr int kOffMisc = kOffBar + kNumBar * 8;
+  static constexpr int kUsed = kOffMisc + 16;
+  // At most two CTAs (two 256-column TMEM allocations) on an SM, one at d = 256.
+  static constexpr int kSmem = HD == 256 || kUsed + 1024 > 102400 ? kUsed + 1024 : 102400;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(HD == 256 || 2 * (kSmem + 4096) <= 233472, "two CTAs per SM");
+  static constexpr uint32_t kColO = 128;
+  static constexpr uint32_t kTmemCols = HD == 256 ? 512 : 256;
+  static constexpr int kMinCtas = HD == 256 ? 1 : 2;
+  // Converter: threads a token's row of codes, tokens a pass, passes a tile.
+  static constexpr int kTpr = HD / 32, kPassTokens = 128 / kTpr, kPasses = kTile / kPassTokens;
+};
+
+__device__ __forceinline__ bool bar_and_128(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// The tiles of a CTA's share, item by item.
+struct Tiles {
+  Kv4Walk<kTile> w;
+  long long u, u_end;
+  int t, first, last;  // tile of the item; the part of it in this share
+
+  __device__ __forceinline__ void begin(const Kv4AttnArgs& a, const Kv4Share& s) {
+    u = s.per * blockIdx.x;
+    u_end = min(s.total, u + s.per);
+    w.seek(a, s, u, kRows);
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    t = first = static_cast<int>(u - w.item);
+    last = static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
+  }
+  // To the next item; false behind the share's end.
+  __device__ __forceinline__ bool next_item(const Kv4AttnArgs& a) {
+    u = w.item + last;
+    if (u >= u_end) return false;
+    w.next(a, kRows);
+    open();
+    return true;
+  }
+};
+
+template <int HD, int GROUP>
+__global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
+    kv4_chunk_kernel(const Kv4AttnArgs a) {
+  using C = Cfg<HD, GROUP>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long scratch[kThreads / 32 + 2];
+  __shared__ float k_unit[kUnits];         // 2^kexp of a tile
+  __shared__ int v_exp[kUnits];
+  __shared__ uint32_t top_param[2][2][4];  // [tile parity][K, V][warp]
+  __shared__ uint8_t odd_v[kUnits][kTile]; // groups of a token's V that are not numbers
+  __shared__ int any_odd[kUnits];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t pad = ((raw_u32 + 1023u) & ~1023u) - raw_u32;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = raw_u32 + pad;
+  const uint32_t bar0 = sb + C::kOffBar;
+  const uint32_t bar_q = bar0;
+  const uint32_t bar_kfull = bar0 + 8, bar_kempty = bar0 + 24, bar_vfull = bar0 + 40,
+                 bar_vempty = bar0 + 56, bar_sfull = bar0 + 72, bar_pfull = bar0 + 88,
+                 bar_odone = bar0 + 104, bar_drain = bar0 + 112;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const Kv4Share share = kv4_share<kTile, kThreads>(a, kRows, 4, scratch);
+  const bool idle = share.per * blockIdx.x >= share.total;
+  if (idle) {
+    if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+
+  if (tid == 0) {
+    mbar_init(bar_q, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_kfull + 8 * s, 4);
+      mbar_init(bar_kempty + 8 * s, 1);
+      mbar_init(bar_vfull + 8 * s, 4);
+      mbar_init(bar_vempty + 8 * s, 1);
+      mbar_init(bar_sfull + 8 * s, 1);
+      mbar_init(bar_pfull + 8 * s, 4);
+    }
+    mbar_init(bar_odone, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // Slots of the extra k-steps that no group uses stay zero.
+  for (int i = tid; i < (C::kQEx + 2 * C::kKEx) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + C::kOffQEx)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Abort ab{a.wait_err, abort_flag};
+  Tiles w;
+  w.begin(a, share);
+
+  if (warp < 4) {
+    // ---------------------------------------------------------- rows
+    const int row = warp * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    int4 record = make_int4(0, 0, 0, 0);
+    bool ok = true, first_item = true;
+    int it = 0;
+    do {
+      const Kv4Walk<kTile>& k = w.w;
+      const bool have = row < k.blk.rows;
+      const int gr = k.blk.row0 + (have ? row : 0);
+      const int t = gr / a.per_kv, head = k.h * a.per_kv + gr - t * a.per_kv;
+      int row_lo = 0, row_hi = have ? k.req.kv : 0;
+      if (have && (a.causal || a.window >= 0)) row_hi = max(min(row_hi, k.blk.pos0 + t + 1), 0);
+      if (a.window >= 0) row_lo = max(k.blk.pos0 + t - min(a.window, 0x3fffffff), 0);
+      const uint32_t seen = static_cast<uint32_t>(max(row_hi - row_lo, 0));
+
+      // Q: the row scaled by a power of two into [2^7, 2^8), in fp16, and the
+      // slots of its sums over the groups.  The products of the item before
+      // have all completed (its O was read), so the tile is free.
+      float row_scale;
+      {
+        const uint16_t* src = a.Q + static_cast<long long>(k.req.start + t) * a.q_ts +
+                              static_cast<long long>(head) * a.q_hs;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint4 x = have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                       __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+        const int et = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7) - 127;  // -127: zero
+        // The power of two is applied in two halves: either alone is in range.
+        const int up = 7 - max(et, -126);
+        const float u0 = pow2i(up / 2), u1 = pow2i(up - up / 2);
+        row_scale = a.scale_log2 * pow2i(-(up / 2)) * pow2i(-(up - up / 2));
+        float sum = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint4 x = have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(in[i] << 16) * u0 * u1;
+            const float hi = __uint_as_float(in[i] & 0xffff0000u) * u0 * u1;
+            sum += lo + hi;
+            out[i] = pack_f16(lo, hi);
+          }
+          *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * C::kQAtom + row * 128 +
+                                    (((c & 7) ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+          if ((c + 1) % (GROUP / 8) == 0) {
+            const int g = c / (GROUP / 8);
+            const __half h = __float2half_rn(sum), l = __float2half_rn(sum - __half2float(h));
+            const __half slot[3] = {h, h, l};
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+              const int kk = 3 * g + e;
+              *reinterpret_cast<__half*>(smem + C::kOffQEx + (row >> 3) * C::kExRow8 + (kk >> 3) * 128 +
+                                         (row & 7) * 16 + (kk & 7) * 2) = slot[e];
+            }
+            sum = 0.f;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q);
+
+      float m_run = -INFINITY, l_run = 0.f;
+      int v_ref = 0;
+      uint32_t nan_groups = 0;
+      for (; w.t < w.last; ++w.t, ++it) {
+        const int bb = it & 1;
+        const uint32_t scol = bb ? 64u : 0u;
+        const int key0 = (k.blk.tile_lo + w.t) * kTile;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_sfull + 8u * bb, (it >> 1) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[2][32];
+        tmem_ld32(tl + scol, sr[0]);
+        tmem_ld32(tl + scol + 32, sr[1]);
+        const float mult = row_scale * k_unit[it & (kUnits - 1)];
+        const int ve = v_exp[it & (kUnits - 1)];
+        tmem_wait_ld();
+        const bool edge = key0 + kTile > k.blk.all_hi || key0 < k.blk.all_lo;
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              sr[c][e] = static_cast<uint32_t>(key0 + 32 * c + e - row_lo) < seen
+                             ? sr[c][e]
+                             : __float_as_uint(-INFINITY);
+          if (any_odd[it & (kUnits - 1)])
+            for (int e = 0; e < kTile; ++e)
+              if (static_cast<uint32_t>(key0 + e - row_lo) < seen)
+                nan_groups |= odd_v[it & (kUnits - 1)][e];
+        }
+        float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mxp[e & 3] = fmaxf(mxp[e & 3], __uint_as_float(sr[c][e]));
+        const float cand = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mult;
+        const bool start = w.t == w.first;
+        const bool up = cand > m_run + kGrow;
+        const float m_new = up ? cand : m_run;
+        const float alpha_l = up ? ex2(m_run - m_new) : 1.f;
+        const float alpha = alpha_l * ex2(static_cast<float>(v_ref - ve));  // V's unit only grows
+        const bool rescale = up || ve != v_ref;
+        const float base = m_new == -INFINITY ? 0.f : kShift - m_new;
+        const uint64_t mult2 = f2_pack(mult, mult), base2 = f2_pack(base, base);
+        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])),
+                             mult2, base2),
+                      x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            pk[e] = pack_f16(p0, p1);
+            sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
+          }
+          tmem_st16(tl + scol + 16 * c, pk);
+        }
+        float z0, z1;
+        f2_unpack(f2_add(sum2[0], sum2[1]), z0, z1);
+        l_run = l_run * alpha_l + (z0 + z1);
+        m_run = m_new;
+        v_ref = ve;
+        if (!start) {
+          // The product of the tile before has to be complete: O may be rescaled
+          // then, and the phase waited for is the only one that can be open
+          // (the next product needs this tile's P).
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_odone, (it - 1) & 1, ab))) {
+            ok = false;
+            break;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tl + C::kColO + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tl + C::kColO + 16 * c, o);
+            }
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_pfull + 8u * bb);
+      }
+      if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_odone, (it - 1) & 1, ab));
+        tc_fence_after();
+      }
+      ok = bar_and_128(1, ok && *abort_flag == 0);
+      if (!ok) break;
+
+      const bool whole = w.first == 0 && w.last == k.blk.tiles;
+      if (w.first == 0 && !whole) record = kv4_split_record(k, share);
+      const float v_up = ex2(static_cast<float>(v_ref));
+      const float top = m_run - kShift;
+      const float f = whole ? (l_run == 0.f ? 0.f : v_up / l_run) : v_up;
+      const long long o_row = static_cast<long long>(k.req.start + t) * a.Hq + head;
+      const long long p_row =
+          (2ll * blockIdx.x + (first_item && w.first > 0 ? 0 : 1)) * kRows + row;
+#pragma unroll 1
+      for (int c = 0; c < HD / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tl + C::kColO + 16 * c, o);
+        tmem_wait_ld();
+        const bool odd = (nan_groups >> (16 * c / GROUP)) & 1;
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = odd ? __int_as_float(0x7fffffff) : __uint_as_float(o[e]) * f;
+        if (!have) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.O + o_row * HD + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            dst[e] = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
+                                pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + p_row * HD + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
+      }
+      if (have) {
+        if (whole)
+          a.L[o_row] = l_run == 0.f ? -INFINITY : (top + log2f(l_run)) * kLn2f;
+        else
+          a.part_stat[p_row] = make_float2(top, l_run);
+      }
+      // O has been read before the next item's products may overwrite it: they
+      // wait for p_full, which this warp signals after this point.
+      tc_fence_before();
+      first_item = false;
+    } while (w.next_item(a));
+    if (tid == 0) a.split[blockIdx.x] = record;
+  } else if (warp < 8) {
+    // ---------------------------------------------------------- codes to tiles
+    const int ct = tid - 128, cw = warp - 4;
+    const int part = ct % C::kTpr;   // 32-channel block
+    const int ptok = ct / C::kTpr;   // token of a pass
+    const int group = part * 32 / GROUP;
+    struct Load {
+      uint4 k[C::kPasses], v[C::kPasses];
+      uint32_t kp[C::kPasses], vp[C::kPasses];
+    };
+    int pages[C::kPasses];
+    int key_next = 0, hi_next = 0;   // tile that `pages` is for
+    bool more = true;
+    // `w` runs two tiles ahead of the conversion: pages, then codes.
+    auto fetch_pages = [&]() {
+      key_next = (w.w.blk.tile_lo + w.t) * kTile;
+      hi_next = w.w.blk.hi;
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int tok = key_next + p * C::kPassTokens + ptok;
+        int pg = 0;
+        if (tok < hi_next) {
+          pg = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages + (tok >> a.lay.page_shift));
+          if (pg < 0 || pg >= a.num_pages) {
+            atomicCAS(a.input_err, 0, 1);
+            pg = 0;
+          }
+        }
+        pages[p] = pg;
+      }
+    };
+    auto fetch_codes = [&](Load& x, int h) {
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int tok = key_next + p * C::kPassTokens + ptok;
+        x.k[p] = make_uint4(0, 0, 0, 0);
+        x.v[p] = x.k[p];
+        x.kp[p] = 0;
+        x.vp[p] = 0;
+        if (tok < hi_next) {
+          const int off = tok & ((1 << a.lay.page_shift) - 1);
+          const uint8_t* rec = a.cache + (static_cast<long long>(pages[p]) * a.Hkv + h) * a.lay.record;
+          const uint8_t* c = rec + off * a.lay.code_row + part * 16;
+          const uint8_t* q = rec + a.lay.k_params + off * a.lay.param_row + group * 4;
+          x.k[p] = __ldg(reinterpret_cast<const uint4*>(c));
+          x.v[p] = __ldg(reinterpret_cast<const uint4*>(c + a.lay.v_codes));
+          x.kp[p] = __ldg(reinterpret_cast<const uint32_t*>(q));
+          x.vp[p] = __ldg(reinterpret_cast<const uint32_t*>(q + (a.lay.v_params - a.lay.k_params)));
+        }
+      }
+    };
+    auto step = [&]() {  // w to its next tile
+      if (++w.t >= w.last) more = w.next_item(a);
+    };
+    // Largest params of a tile, numbers only: [parity][K, V][warp].
+    auto post_top = [&](const Load& x, int parity) {
+      uint32_t tk = 0, tv = 0;
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        if (!odd_param(x.kp[p])) tk = __vmaxu2(tk, x.kp[p] & 0x7fff7fffu);
+        if (!odd_param(x.vp[p])) tv = __vmaxu2(tv, x.vp[p] & 0x7fff7fffu);
+      }
+      const uint32_t km = __reduce_max_sync(0xffffffffu, tk >> 16), ks = __reduce_max_sync(0xffffffffu, tk & 0xffffu);
+      const uint32_t vm = __reduce_max_sync(0xffffffffu, tv >> 16), vs = __reduce_max_sync(0xffffffffu, tv & 0xffffu);
+      if (lane == 0) {
+        top_param[parity][0][cw] = (km << 16) | ks;
+        top_param[parity][1][cw] = (vm << 16) | vs;
+      }
+    };
+    // |minimum| < 2^(e + 14), scale < 2^(e + 10)
+    auto unit_of = [&](int parity, int side) -> int {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, top_param[parity][side][i]);
+      const int em = static_cast<int>(m >> 23), es = static_cast<int>((m >> 7) & 255);
+      return max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
+    };
+
+    Load cur, nxt;
+    int h_next = w.w.h;
+    fetch_pages();
+    fetch_codes(cur, h_next);
+    int key0 = key_next;
+    int all_hi = w.w.blk.all_hi, all_lo = w.w.blk.all_lo;
+    bool first = true;   // the tile is its item's first
+    int v_run = 0;       // V's unit so far in the item
+    step();
+    bool nxt_ok = more;
+    if (nxt_ok) {
+      h_next = w.w.h;
+      fetch_pages();
+    }
+    post_top(cur, 0);
+    bool ok = true;
+    for (int it = 0; it >= 0; ++it) {
+      const int st = it & 1, un = it & (kUnits - 1);
+      // The next tile's codes, and the pages of the one after it.
+      const int key_n = key_next;
+      int all_hi_n = 0, all_lo_n = 0;
+      bool first_n = false;
+      const bool have_next = nxt_ok;
+      if (have_next) {
+        first_n = w.t == w.first;
+        all_hi_n = w.w.blk.all_hi;
+        all_lo_n = w.w.blk.all_lo;
+        fetch_codes(nxt, h_next);
+        step();
+        nxt_ok = more;
+        if (nxt_ok) {
+          h_next = w.w.h;
+          fetch_pages();
+        }
+      }
+      // All four warps posted this tile's largest params (and, on the way, read
+      // the last tile's, so that those may be overwritten).
+      // Every warp passes here once a tile, so that one that gave up on a wait
+      // takes the others along.
+      ok = bar_and_128(2, ok);
+      if (!ok) break;
+      const int ke = unit_of(it & 1, 0);
+      v_run = first ? unit_of(it & 1, 1) : max(v_run, unit_of(it & 1, 1));
+      const int ve = v_run;
+      if (ct == 0) {
+        k_unit[un] = pow2i(ke);
+        v_exp[un] = ve;
+        any_odd[un] = 0;
+      }
+      const float kd = pow2i(-ke), vd = pow2i(-ve);
+      const bool edge = key0 + kTile > all_hi || key0 < all_lo;
+      if (edge) asm volatile("bar.sync 2, 128;" ::: "memory");  // any_odd is 0
+
+      if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar_kempty + 8u * st, ((it >> 1) & 1) ^ 1, ab))) {
+        ok = false;
+        if (!have_next) break;
+        continue;
+      }
+      // A word of codes is 16 bytes of the tile.  Threads two apart write to the
+      // same banks of neighbouring atoms: every other pair takes its words in
+      // another order.
+      const int flip = (part >> 1) & 1;
+      uint8_t* kt = smem + C::kOffK + st * C::kTileBytes;
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int tok = p * C::kPassTokens + ptok;
+        const float s = param_scale(cur.kp[p]) * kd;
+        const float m = fmaf(8.f, s, param_min(cur.kp[p]) * kd);
+        const uint32_t s2 = pack_f16(s, s);
+        const uint32_t w0 = flip ? cur.k[p].z : cur.k[p].x, w1 = flip ? cur.k[p].w : cur.k[p].y;
+        const uint32_t w2 = flip ? cur.k[p].x : cur.k[p].z, w3 = flip ? cur.k[p].y : cur.k[p].w;
+        const uint32_t ww[4] = {w0, w1, w2, w3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int chunk = part * 4 + (i ^ (flip << 1));
+          uint4 o;
+          o.x = mul_f16x2(codes_m8(ww[i], 0), s2);
+          o.y = mul_f16x2(codes_m8(ww[i], 1), s2);
+          o.z = mul_f16x2(codes_m8(ww[i], 2), s2);
+          o.w = mul_f16x2(codes_m8(ww[i], 3), s2);
+          *reinterpret_cast<uint4*>(kt + (chunk >> 3) * C::kAtom + tok * 128 +
+                                    (((chunk & 7) ^ (tok & 7)) << 4)) = o;
+        }
+        if (GROUP == 32 || (part & 1) == 0) {
+          const __half h = __float2half_rn(m), l = __float2half_rn(m - __half2float(h));
+          const __half slot[3] = {h, l, h};
+          uint8_t* ex = smem + C::kOffKEx + st * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const int kk = 3 * group + e;
+            *reinterpret_cast<__half*>(ex + (kk >> 3) * 128 + (kk & 7) * 2) = slot[e];
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_kfull + 8u * st);
+
+      if (edge) {
+        // Values that are not numbers, where some row does not see them: left
+        // out of the product; the rows that see them add them by themselves.
+#pragma unroll
+        for (int p = 0; p < C::kPasses; ++p) {
+          const int tok = p * C::kPassTokens + ptok;
+          const bool odd = odd_param(cur.vp[p]);
+          // the token's threads are side by side in the warp
+          uint32_t bits = odd ? 1u << group : 0u;
+#pragma unroll
+          for (int d = 1; d < C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
+          if (part == 0) odd_v[un][tok] = static_cast<uint8_t>(bits);
+          if (bits) any_odd[un] = 1;
+          if (odd) cur.vp[p] = 0;
+        }
+      }
+      if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar_vempty + 8u * st, ((it >> 1) & 1) ^ 1, ab))) {
+        ok = false;
+        if (!have_next) break;
+        continue;
+      }
+      uint8_t* vt = smem + C::kOffV + st * C::kTileBytes;
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int tok = p * C::kPassTokens + ptok;
+        const float s = param_scale(cur.vp[p]) * vd;
+        const float m = fmaf(8.f, s, param_min(cur.vp[p]) * vd);
+        const uint32_t s2 = pack_f16(s, s), m2 = pack_f16(m, m);
+        const uint32_t w0 = flip ? cur.v[p].z : cur.v[p].x, w1 = flip ? cur.v[p].w : cur.v[p].y;
+        const uint32_t w2 = flip ? cur.v[p].x : cur.v[p].z, w3 = flip ? cur.v[p].y : cur.v[p].w;
+        const uint32_t ww[4] = {w0, w1, w2, w3};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int chunk = part * 4 + (i ^ (flip << 1));
+          uint4 o;
+          o.x = fma_f16x2(codes_m8(ww[i], 0), s2, m2);
+          o.y = fma_f16x2(codes_m8(ww[i], 1), s2, m2);
+          o.z = fma_f16x2(codes_m8(ww[i], 2), s2, m2);
+          o.w = fma_f16x2(codes_m8(ww[i], 3), s2, m2);
+          *reinterpret_cast<uint4*>(vt + (chunk >> 3) * C::kAtom + tok * 128 +
+                                    (((chunk & 7) ^ (tok & 7)) << 4)) = o;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_vfull + 8u * st);
+      if (!have_next) break;
+      post_top(nxt, (it + 1) & 1);
+      cur = nxt;
+      key0 = key_n;
+      all_hi = all_hi_n;
+      all_lo = all_lo_n;
+      first = first_n;
+    }
+  } else if (lane == 0) {
+    // ---------------------------------------------------------- products
+    constexpr uint32_t idS = idesc_f16(kRows, kTile, false);
+    constexpr uint32_t idO = idesc_f16(kRows, HD, true);
+    constexpr int kD = HD / 16, kC = kTile / 16;
+    uint64_t aQ[kD];
+    {
+      const uint64_t d0 = sdesc_sw128(sb + C::kOffQ, 16, 1024);
+#pragma unroll
+      for (int k = 0; k < kD; ++k) aQ[k] = sdesc_add(d0, (k >> 2) * C::kQAtom + (k & 3) * 32);
+    }
+    const uint64_t aX = sdesc_plain(sb + C::kOffQEx, 128, C::kExRow8);
+    bool ok = true;
+    int it = 0, item = 0;
+    bool prev_first = false;  // was tile it - 1 its item's first?
+    auto issue_pv = [&](int jj, bool first) -> bool {
+      const int bb = jj & 1;
+      if (!mbar_wait(bar_pfull + 8u * bb, (jj >> 1) & 1, ab)) return false;
+      if (!mbar_wait(bar_vfull + 8u * bb, (jj >> 1) & 1, ab)) return false;
+      tc_fence_after();
+      uint64_t b[kC];
+      uint32_t p[kC];
+      const uint64_t d0 = sdesc_sw128(sb + C::kOffV + bb * C::kTileBytes, C::kAtom, 1024);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        b[k] = sdesc_add(d0, k * 2048);
+        p[k] = tmem + (bb ? 64u : 0u) + 8u * k;
+      }
+      mma_ts_k(tmem + C::kColO, p, b, idO, first ? 0u : 1u);
+      mma_commit(bar_odone);
+      mma_commit(bar_vempty + 8u * bb);
+      return true;
+    };
+    do {
+      // The rows put an item's Q in place once they have read the O before, for
+      // which the last product has to be issued first.
+      if (it > 0 && !issue_pv(it - 1, prev_first)) break;
+      if (!mbar_wait(bar_q, item & 1, ab)) break;
+      ++item;
+      for (; w.t < w.last; ++w.t, ++it) {
+        const int bb = it & 1;
+        // S over P of two tiles before: its product has to be complete.  (At an
+        // item's first tile the wait for Q has shown more than that, and the
+        // phase waited for here may be over already.)
+        if (it >= 2 && w.t > w.first && !mbar_wait(bar_odone, (it - 2) & 1, ab)) { ok = false; break; }
+        if (!mbar_wait(bar_kfull + 8u * bb, (it >> 1) & 1, ab)) { ok = false; break; }
+        tc_fence_after();
+        {
+          uint64_t b[kD];
+          const uint64_t d0 = sdesc_sw128(sb + C::kOffK + bb * C::kTileBytes, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kD; ++k) b[k] = sdesc_add(d0, (k >> 2) * C::kAtom + (k & 3) * 32);
+          mma_ss_k(tmem + (bb ? 64u : 0u), aQ, b, idS, 0u);
+          const uint64_t x0 = sdesc_plain(sb + C::kOffKEx + bb * C::kKEx, 128, C::kExRow8);
+#pragma unroll
+          for (int k = 0; k < C::kExSteps; ++k)
+            mma_ss(tmem + (bb ? 64u : 0u), sdesc_add(aX, k * 256), sdesc_add(x0, k * 256), idS, 1u);
+        }
+        mma_commit(bar_sfull + 8u * bb);
+        mma_commit(bar_kempty + 8u * bb);
+        if (w.t > w.first && !issue_pv(it - 1, w.t - 1 == w.first)) { ok = false; break; }
+      }
+      prev_first = w.last - 1 == w.first;
+    } while (ok && w.next_item(a));
+    if (ok && it > 0 && *abort_flag == 0) issue_pv(it - 1, prev_first);
+    mma_commit(bar_drain);
+    mbar_wait_drain(bar_drain, 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int HD, int GROUP>
+cudaError_t launch_chunk(const Kv4AttnArgs& a, cudaStream_t stream, int* ctas) {
+  using C = Cfg<HD, GROUP>;
+  static std::atomic<bool> ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kv4_chunk_kernel<HD, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  const int sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  *ctas = C::kMinCtas * sms < kKv4MaxChunkCtas ? C::kMinCtas * sms : kKv4MaxChunkCtas;
+  kv4_chunk_kernel<HD, GROUP><<<*ctas, kThreads, C::kSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_chunk(int d, int group, const Kv4AttnArgs& a, cudaStream_t stream, int* ctas) {
+  const bool g32 = group == 32;
+  switch (d) {
+    case 64: return g32 ? launch_chunk<64, 32>(a, stream, ctas) : launch_chunk<64, 64>(a, stream, ctas);
+    case 128: return g32 ? launch_chunk<128, 32>(a, stream, ctas) : launch_chunk<128, 64>(a, stream, ctas);
+    case 256: return g32 ? launch_chunk<256, 32>(a, stream, ctas) : launch_chunk<256, 64>(a, stream, ctas);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fa
