@@ -90,10 +90,9 @@ struct Kv4AttnArgs {
 // CTAs of a launch never exceed these, so that the workspace's size does not
 // depend on the device.
 constexpr int kKv4MaxCtas = 640;       // few query rows (kv4_attn.cu)
-constexpr int kKv4MaxChunkCtas = 320;  // many (kv4_chunk.cu)
-constexpr int kKv4ChunkRows = 128;
+constexpr int kKv4MaxChunkCtas = 160;  // many (kv4_chunk.cu)
 // Query rows of one CTA's block, given the most rows (queries x heads per K/V
-// head) a request may have; kKv4ChunkRows selects the kernel for many.
+// head) a request may have; 128 and more select the kernel for many.
 int kv4_attn_rows(int d, int rows);
 size_t kv4_attn_workspace(int d, int rows);
 cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cudaStream_t stream);

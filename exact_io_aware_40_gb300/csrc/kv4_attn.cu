@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     kv4_merge_kernel(const Kv4AttnArgs a, int block_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 rec = a.split[blockIdx.x];
-  const int rows = rec.z & 255, h = rec.z >> 8;
+  const int rows = rec.z & 511, h = rec.z >> 9;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -750,12 +750,13 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
 
 template <int HD, int GROUP>
 cudaError_t launch_attn_rows(const Kv4AttnArgs& a, cudaStream_t stream) {
-  switch (kv4_attn_rows(HD, a.max_q * a.per_kv)) {
-    case kKv4ChunkRows: {
-      int ctas = 0;
-      const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
-      return e != cudaSuccess ? e : launch_merge<HD>(a, ctas, kKv4ChunkRows, stream);
-    }
+  const int block = kv4_attn_rows(HD, a.max_q * a.per_kv);
+  if (block >= 128) {
+    int ctas = 0;
+    const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
+    return e != cudaSuccess ? e : launch_merge<HD>(a, ctas, block, stream);
+  }
+  switch (block) {
     case 8: return launch_attn<HD, GROUP, 1>(a, stream);
     case 16: return launch_attn<HD, GROUP, 2>(a, stream);
     default:
@@ -774,13 +775,13 @@ int kv4_attn_rows(int d, int rows) {
   if (rows <= 8) return 8;
   if (rows <= 16) return 16;
   if (rows <= 32 && d != 256) return 32;  // d = 256: 32 rows of O would not fit the registers
-  return kKv4ChunkRows;
+  return d == 256 ? 128 : 256;
 }
 
 namespace {
 size_t part_rows(int d, int rows) {  // rows of all partial results
   const int block = kv4_attn_rows(d, rows);
-  return 2 * static_cast<size_t>(block == kKv4ChunkRows ? kKv4MaxChunkCtas : kKv4MaxCtas) * block;
+  return 2 * static_cast<size_t>(block >= 128 ? kKv4MaxChunkCtas : kKv4MaxCtas) * block;
 }
 }  // namespace
 
@@ -800,7 +801,7 @@ cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cu
   a.part_o = reinterpret_cast<float*>(ws);
   // With at most four tiles to an item, cutting it saves less than the merge
   // costs (one more launch).
-  a.whole_items = kv4_attn_rows(d, a.max_q * a.per_kv) != kKv4ChunkRows &&
+  a.whole_items = kv4_attn_rows(d, a.max_q * a.per_kv) < 128 &&
                   (static_cast<long long>(a.max_pages) << a.lay.page_shift) <= 4 * kTile;
   const bool g32 = group == 32;
   switch (d) {

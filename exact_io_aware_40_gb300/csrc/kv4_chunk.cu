@@ -1,16 +1,17 @@
 // kv4_chunk.cu -- attention over the paged 4-bit cache for many query rows: a
 // chunk of a prompt, or drafted tokens of many query heads.
 //
-// One CTA takes blocks of 128 query rows (queries x query heads of one K/V head)
-// and walks its share of the tiles of 64 tokens (kv4_sched.cuh).  Both products
-// run on the tensor cores out of tensor memory as in the bf16 forward (S double
-// buffered, P over S as the A operand of P V, O resident); what differs is where
-// K and V come from:
-//   - warps 4-7 read a tile's codes and params (16 bytes a thread, a row's
-//     threads side by side) one tile ahead into registers and write them as fp16
-//     tiles in the 128-byte-swizzled layout the products take;
-//   - warps 0-3 (thread = row = TMEM lane) load Q, do the softmax and write O;
-//   - one thread of warp 8 issues the products.
+// One CTA per SM takes blocks of 256 query rows (128 at d = 256; queries x query
+// heads of one K/V head) and walks its share of the tiles of 64 tokens
+// (kv4_sched.cuh).  Both products run on the tensor cores out of tensor memory as
+// in the bf16 forward (S double buffered, P over S as the A operand of P V, O
+// resident); what differs is where K and V come from:
+//   - the converter, four warps, copies a tile's codes and params some tiles
+//     ahead (cp.async; a thread's own 16 bytes, so nobody waits for anybody) and
+//     writes them as fp16 tiles in the 128-byte-swizzled layout the products take;
+//   - a warpgroup for each 128 rows (thread = row = TMEM lane) loads Q, does the
+//     softmax and writes O; the two share every converted tile;
+//   - one thread issues the products.
 //
 // K.  (code - 8) * scale has at most 8 + 3 significant bits and so is exact in
 // fp16, as Q is (8 bits) after a scaling of each row by a power of two.  The
@@ -23,10 +24,8 @@
 // fits the tile's largest param.  K's unit multiplies the tile's scores; V's goes
 // into the exponent of P, whose reference then includes the largest unit so far.
 //
-// Bound: the tensor cores (4 d FLOP a score) and, near it, the instructions of
-// the two warpgroups: a tile costs about 15 for eight codes and 3.5 for a score
-// against 616 clocks of products at d = 128.  Two CTAs per SM (d <= 128) cover
-// each other's waits.
+// Bound: issue slots (about 17 instructions for eight codes, 3.5 for a score)
+// and, near them, the tensor cores.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -39,9 +38,8 @@
 namespace fa {
 namespace {
 
-constexpr int kRows = 128;
+constexpr int kRows = 128;  // rows of a warpgroup
 constexpr int kTile = 64;
-constexpr int kThreads = 288;
 constexpr float kGrow = 4.f;
 constexpr float kShift = 10.f;
 constexpr float kLn2f = 0.693147180559945309f;
@@ -97,35 +95,60 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, ui
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int HD, int GROUP>
 struct Cfg {
   static constexpr int kGroups = HD / GROUP;
+  static constexpr int kCodeRow = HD / 2, kParamRow = 4 * kGroups;
   static constexpr int kAtoms = HD / 64;
+  static constexpr int kBlocks = HD == 256 ? 1 : 2;      // warpgroups of rows
+  static constexpr int kBlockRows = kBlocks * kRows;
+  static constexpr int kThreads = 128 * (kBlocks + 2);   // + converter, products
   static constexpr int kQAtom = kRows * 128, kQTile = kAtoms * kQAtom;
   static constexpr int kAtom = kTile * 128, kTileBytes = kAtoms * kAtom;  // K or V tile
+  static constexpr int kKSt = HD == 256 ? 1 : 2, kVSt = 2;
   // Extra slots: three for each group, in k-steps of 16.
   static constexpr int kExSteps = (3 * kGroups + 15) / 16;
   static constexpr int kExRow8 = kExSteps * 256;  // bytes of eight rows
   static constexpr int kQEx = kRows / 8 * kExRow8, kKEx = kTile / 8 * kExRow8;
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kQTile;
-  static constexpr int kOffV = kOffK + 2 * kTileBytes;
-  static constexpr int kOffQEx = kOffV + 2 * kTileBytes;
-  static constexpr int kOffKEx = kOffQEx + kQEx;
-  static constexpr int kOffBar = kOffKEx + 2 * kKEx;
-  // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, drain
-  static constexpr int kNumBar = 15;
-  static constexpr int kOffMisc = kOffBar + kNumBar * 8;
-  static constexpr int kUsed = kOffMisc + 16;
-  // At most two CTAs (two 256-column TMEM allocations) on an SM, one at d = 256.
-  static constexpr int kSmem = HD == 256 || kUsed + 1024 > 102400 ? kUsed + 1024 : 102400;
-  static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(HD == 256 || 2 * (kSmem + 4096) <= 233472, "two CTAs per SM");
-  static constexpr uint32_t kColO = 128;
-  static constexpr uint32_t kTmemCols = HD == 256 ? 512 : 256;
-  static constexpr int kMinCtas = HD == 256 ? 1 : 2;
-  // Converter: threads a token's row of codes, tokens a pass, passes a tile.
+  // Converter: threads a token's row of codes, tokens a pass, passes a tile;
+  // tiles of codes in flight or in use, each thread's own 16 + 16 + 4 + 4 bytes
+  // a pass.
   static constexpr int kTpr = HD / 32, kPassTokens = 128 / kTpr, kPasses = kTile / kPassTokens;
+  static constexpr int kRing = HD == 256 ? 2 : 4;
+  static constexpr int kRingTile = kPasses * 128 * 40;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kBlocks * kQTile;
+  static constexpr int kOffV = kOffK + kKSt * kTileBytes;
+  static constexpr int kOffQEx = kOffV + kVSt * kTileBytes;
+  static constexpr int kOffKEx = kOffQEx + kBlocks * kQEx;
+  static constexpr int kOffRing = kOffKEx + kKSt * kKEx;
+  static constexpr int kOffBar = kOffRing + kRing * kRingTile;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], drain, then for each block of
+  // rows q_full, s_full[2], p_full[2], o_done
+  static constexpr int kNumBar = 9 + 6 * kBlocks;
+  static constexpr int kOffMisc = kOffBar + kNumBar * 8;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  static_assert(kSmem <= 230000, "shared memory budget");
+  // TMEM: S buffers of a block side by side, then every block's O.
+  static constexpr uint32_t kColO = 128 * kBlocks;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kColO + kBlocks * HD <= kTmemCols, "tensor memory budget");
+  // Registers a thread of the warpgroups (rows, converter, products) out of the
+  // launch's.
+  static constexpr int kLaunchRegs = kBlocks == 2 ? 128 : 168;
+  static constexpr int kRowRegs = kBlocks == 2 ? 152 : 200;
+  static constexpr int kConvRegs = kBlocks == 2 ? 112 : 168;
+  static constexpr int kMmaRegs = kBlocks == 2 ? 96 : 128;
+  static_assert(kBlocks * kRowRegs + kConvRegs + kMmaRegs <= (kBlocks + 2) * kLaunchRegs, "register split");
 };
 
 __device__ __forceinline__ bool bar_and_128(int id, bool pred) {
@@ -142,6 +165,7 @@ __device__ __forceinline__ bool bar_and_128(int id, bool pred) {
 }
 
 // The tiles of a CTA's share, item by item.
+template <int kBlockRows>
 struct Tiles {
   Kv4Walk<kTile> w;
   long long u, u_end;
@@ -150,7 +174,7 @@ struct Tiles {
   __device__ __forceinline__ void begin(const Kv4AttnArgs& a, const Kv4Share& s) {
     u = s.per * blockIdx.x;
     u_end = min(s.total, u + s.per);
-    w.seek(a, s, u, kRows);
+    w.seek(a, s, u, kBlockRows);
     open();
   }
   __device__ __forceinline__ void open() {
@@ -161,16 +185,25 @@ struct Tiles {
   __device__ __forceinline__ bool next_item(const Kv4AttnArgs& a) {
     u = w.item + last;
     if (u >= u_end) return false;
-    w.next(a, kRows);
+    w.next(a, kBlockRows);
     open();
     return true;
   }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(have ? 4 : 0)
+               : "memory");
+}
+
 template <int HD, int GROUP>
-__global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
-    kv4_chunk_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a) {
   using C = Cfg<HD, GROUP>;
+  constexpr int kThreads = C::kThreads, kConv = 4 * C::kBlocks, kMma = kConv + 4;  // first warps
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kThreads / 32 + 2];
   __shared__ float k_unit[kUnits];         // 2^kexp of a tile
@@ -178,47 +211,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
   __shared__ uint32_t top_param[2][2][4];  // [tile parity][K, V][warp]
   __shared__ uint8_t odd_v[kUnits][kTile]; // groups of a token's V that are not numbers
   __shared__ int any_odd[kUnits];
+  __shared__ int meta[8];                  // of the converter's tiles: bit 0 edge, bit 1 item's first
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t pad = ((raw_u32 + 1023u) & ~1023u) - raw_u32;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sb = raw_u32 + pad;
   const uint32_t bar0 = sb + C::kOffBar;
-  const uint32_t bar_q = bar0;
-  const uint32_t bar_kfull = bar0 + 8, bar_kempty = bar0 + 24, bar_vfull = bar0 + 40,
-                 bar_vempty = bar0 + 56, bar_sfull = bar0 + 72, bar_pfull = bar0 + 88,
-                 bar_odone = bar0 + 104, bar_drain = bar0 + 112;
+  const uint32_t bar_kfull = bar0, bar_kempty = bar0 + 16, bar_vfull = bar0 + 32,
+                 bar_vempty = bar0 + 48, bar_drain = bar0 + 64;
+  auto bar_q = [&](int g) { return bar0 + 72u + 48u * g; };
+  auto bar_sfull = [&](int g, int b) { return bar0 + 80u + 48u * g + 8u * b; };
+  auto bar_pfull = [&](int g, int b) { return bar0 + 96u + 48u * g + 8u * b; };
+  auto bar_odone = [&](int g) { return bar0 + 112u + 48u * g; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const Kv4Share share = kv4_share<kTile, kThreads>(a, kRows, 4, scratch);
-  const bool idle = share.per * blockIdx.x >= share.total;
-  if (idle) {
+  const Kv4Share share = kv4_share<kTile, kThreads>(a, C::kBlockRows, 4, scratch);
+  if (share.per * blockIdx.x >= share.total) {
     if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
 
   if (tid == 0) {
-    mbar_init(bar_q, 4);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_kfull + 8 * s, 4);
       mbar_init(bar_kempty + 8 * s, 1);
       mbar_init(bar_vfull + 8 * s, 4);
       mbar_init(bar_vempty + 8 * s, 1);
-      mbar_init(bar_sfull + 8 * s, 1);
-      mbar_init(bar_pfull + 8 * s, 4);
     }
-    mbar_init(bar_odone, 1);
     mbar_init(bar_drain, 1);
+    for (int g = 0; g < C::kBlocks; ++g) {
+      mbar_init(bar_q(g), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar_sfull(g, b), 1);
+        mbar_init(bar_pfull(g, b), 4);
+      }
+      mbar_init(bar_odone(g), 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   // Slots of the extra k-steps that no group uses stay zero.
-  for (int i = tid; i < (C::kQEx + 2 * C::kKEx) / 16; i += kThreads)
+  for (int i = tid; i < (C::kBlocks * C::kQEx + C::kKSt * C::kKEx) / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + C::kOffQEx)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (warp == 8) {
+  if (warp == kMma) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -227,20 +266,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Abort ab{a.wait_err, abort_flag};
-  Tiles w;
+  Tiles<C::kBlockRows> w;
   w.begin(a, share);
 
-  if (warp < 4) {
+  if (warp < kConv) {
     // ---------------------------------------------------------- rows
-    const int row = warp * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    regs_inc<C::kRowRegs>();
+    const int g = warp >> 2;                 // block of 128 rows
+    const int row = (warp & 3) * 32 + lane;  // of the block
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128u * g;  // S
+    const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kColO + HD * g;
+    uint8_t* sq = smem + C::kOffQ + g * C::kQTile;
+    uint8_t* sqx = smem + C::kOffQEx + g * C::kQEx;
     int4 record = make_int4(0, 0, 0, 0);
     bool ok = true, first_item = true;
-    int it = 0;
+    int tile = 0;  // of the share
+    int it = 0;    // of this block of rows: the tiles of the items that reach it
     do {
-      const Kv4Walk<kTile>& k = w.w;
-      const bool have = row < k.blk.rows;
-      const int gr = k.blk.row0 + (have ? row : 0);
+      const auto& k = w.w;
+      const bool whole = w.first == 0 && w.last == k.blk.tiles;
+      if (w.first == 0 && !whole) record = kv4_split_record(k, share);
+      if (k.blk.rows <= kRows * g) {  // nothing for these rows
+        tile += w.last - w.first;
+        first_item = false;
+        continue;
+      }
+      const bool have = kRows * g + row < k.blk.rows;
+      const int gr = k.blk.row0 + (have ? kRows * g + row : 0);
       const int t = gr / a.per_kv, head = k.h * a.per_kv + gr - t * a.per_kv;
       int row_lo = 0, row_hi = have ? k.req.kv : 0;
       if (have && (a.causal || a.window >= 0)) row_hi = max(min(row_hi, k.blk.pos0 + t + 1), 0);
@@ -279,16 +331,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
             sum += lo + hi;
             out[i] = pack_f16(lo, hi);
           }
-          *reinterpret_cast<uint4*>(smem + C::kOffQ + (c / 8) * C::kQAtom + row * 128 +
+          *reinterpret_cast<uint4*>(sq + (c / 8) * C::kQAtom + row * 128 +
                                     (((c & 7) ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
           if ((c + 1) % (GROUP / 8) == 0) {
-            const int g = c / (GROUP / 8);
+            const int grp = c / (GROUP / 8);
             const __half h = __float2half_rn(sum), l = __float2half_rn(sum - __half2float(h));
             const __half slot[3] = {h, h, l};
 #pragma unroll
             for (int e = 0; e < 3; ++e) {
-              const int kk = 3 * g + e;
-              *reinterpret_cast<__half*>(smem + C::kOffQEx + (row >> 3) * C::kExRow8 + (kk >> 3) * 128 +
+              const int kk = 3 * grp + e;
+              *reinterpret_cast<__half*>(sqx + (row >> 3) * C::kExRow8 + (kk >> 3) * 128 +
                                          (row & 7) * 16 + (kk & 7) * 2) = slot[e];
             }
             sum = 0.f;
@@ -297,25 +349,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_q);
+      if (lane == 0) mbar_arrive(bar_q(g));
 
       float m_run = -INFINITY, l_run = 0.f;
       int v_ref = 0;
       uint32_t nan_groups = 0;
-      for (; w.t < w.last; ++w.t, ++it) {
-        const int bb = it & 1;
-        const uint32_t scol = bb ? 64u : 0u;
+      for (; w.t < w.last; ++w.t, ++it, ++tile) {
+        const int bb = it & 1, un = tile & (kUnits - 1);
+        const uint32_t scol = tl + (bb ? 64u : 0u);
         const int key0 = (k.blk.tile_lo + w.t) * kTile;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_sfull + 8u * bb, (it >> 1) & 1, ab))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_sfull(g, bb), (it >> 1) & 1, ab))) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t sr[2][32];
-        tmem_ld32(tl + scol, sr[0]);
-        tmem_ld32(tl + scol + 32, sr[1]);
-        const float mult = row_scale * k_unit[it & (kUnits - 1)];
-        const int ve = v_exp[it & (kUnits - 1)];
+        tmem_ld32(scol, sr[0]);
+        tmem_ld32(scol + 32, sr[1]);
+        const float mult = row_scale * k_unit[un];
+        const int ve = v_exp[un];
         tmem_wait_ld();
         const bool edge = key0 + kTile > k.blk.all_hi || key0 < k.blk.all_lo;
         if (edge) {
@@ -326,10 +378,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
               sr[c][e] = static_cast<uint32_t>(key0 + 32 * c + e - row_lo) < seen
                              ? sr[c][e]
                              : __float_as_uint(-INFINITY);
-          if (any_odd[it & (kUnits - 1)])
+          if (any_odd[un])
             for (int e = 0; e < kTile; ++e)
-              if (static_cast<uint32_t>(key0 + e - row_lo) < seen)
-                nan_groups |= odd_v[it & (kUnits - 1)][e];
+              if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= odd_v[un][e];
         }
         float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -359,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
             pk[e] = pack_f16(p0, p1);
             sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
           }
-          tmem_st16(tl + scol + 16 * c, pk);
+          tmem_st16(scol + 16 * c, pk);
         }
         float z0, z1;
         f2_unpack(f2_add(sum2[0], sum2[1]), z0, z1);
@@ -370,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
           // The product of the tile before has to be complete: O may be rescaled
           // then, and the phase waited for is the only one that can be open
           // (the next product needs this tile's P).
-          if (!__all_sync(0xffffffffu, mbar_wait(bar_odone, (it - 1) & 1, ab))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_odone(g), (it - 1) & 1, ab))) {
             ok = false;
             break;
           }
@@ -379,38 +430,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
               uint32_t o[16];
-              tmem_ld16(tl + C::kColO + 16 * c, o);
+              tmem_ld16(to + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(tl + C::kColO + 16 * c, o);
+              tmem_st16(to + 16 * c, o);
             }
           }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_pfull + 8u * bb);
+        if (lane == 0) mbar_arrive(bar_pfull(g, bb));
       }
       if (ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_odone, (it - 1) & 1, ab));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_odone(g), (it - 1) & 1, ab));
         tc_fence_after();
       }
-      ok = bar_and_128(1, ok && *abort_flag == 0);
+      ok = bar_and_128(1 + g, ok && *abort_flag == 0);
       if (!ok) break;
 
-      const bool whole = w.first == 0 && w.last == k.blk.tiles;
-      if (w.first == 0 && !whole) record = kv4_split_record(k, share);
       const float v_up = ex2(static_cast<float>(v_ref));
       const float top = m_run - kShift;
       const float f = whole ? (l_run == 0.f ? 0.f : v_up / l_run) : v_up;
       const long long o_row = static_cast<long long>(k.req.start + t) * a.Hq + head;
       const long long p_row =
-          (2ll * blockIdx.x + (first_item && w.first > 0 ? 0 : 1)) * kRows + row;
+          (2ll * blockIdx.x + (first_item && w.first > 0 ? 0 : 1)) * C::kBlockRows + kRows * g + row;
 #pragma unroll 1
       for (int c = 0; c < HD / 16; ++c) {
         uint32_t o[16];
-        tmem_ld16(tl + C::kColO + 16 * c, o);
+        tmem_ld16(to + 16 * c, o);
         tmem_wait_ld();
         const bool odd = (nan_groups >> (16 * c / GROUP)) & 1;
         float x[16];
@@ -441,171 +490,151 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
       first_item = false;
     } while (w.next_item(a));
     if (tid == 0) a.split[blockIdx.x] = record;
-  } else if (warp < 8) {
+  } else if (warp < kMma) {
     // ---------------------------------------------------------- codes to tiles
-    const int ct = tid - 128, cw = warp - 4;
+    if constexpr (C::kConvRegs < C::kLaunchRegs) regs_dec<C::kConvRegs>();
+    const int ct = tid - 32 * kConv, cw = warp - kConv;
     const int part = ct % C::kTpr;   // 32-channel block
     const int ptok = ct / C::kTpr;   // token of a pass
     const int group = part * 32 / GROUP;
-    struct Load {
-      uint4 k[C::kPasses], v[C::kPasses];
-      uint32_t kp[C::kPasses], vp[C::kPasses];
+    const int total = static_cast<int>(w.u_end - w.u);
+    // This thread's place in the ring: K codes, V codes, K params, V params of
+    // pass p of tile n at ring16(n, p), + 2048, ...
+    uint8_t* ring = smem + C::kOffRing;
+    auto ring16 = [&](int n, int p, int side) {
+      return (n % C::kRing) * C::kRingTile + p * 128 * 40 + side * 2048 + ct * 16;
     };
-    int pages[C::kPasses];
-    int key_next = 0, hi_next = 0;   // tile that `pages` is for
-    bool more = true;
-    // `w` runs two tiles ahead of the conversion: pages, then codes.
-    auto fetch_pages = [&]() {
-      key_next = (w.w.blk.tile_lo + w.t) * kTile;
-      hi_next = w.w.blk.hi;
+    auto ring4 = [&](int n, int p, int side) {
+      return (n % C::kRing) * C::kRingTile + p * 128 * 40 + 4096 + side * 512 + ct * 4;
+    };
+    int pages[C::kPasses];  // of the tile w stands at, the next to be copied
+    auto locate = [&]() {
+      const int key = (w.w.blk.tile_lo + w.t) * kTile;
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        const int tok = key_next + p * C::kPassTokens + ptok;
-        int pg = 0;
-        if (tok < hi_next) {
-          pg = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages + (tok >> a.lay.page_shift));
-          if (pg < 0 || pg >= a.num_pages) {
-            atomicCAS(a.input_err, 0, 1);
-            pg = 0;
-          }
-        }
-        pages[p] = pg;
+        const int tok = key + p * C::kPassTokens + ptok;
+        pages[p] = -1;
+        if (tok < w.w.blk.hi)
+          pages[p] = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages +
+                           (tok >> a.lay.page_shift));
       }
     };
-    auto fetch_codes = [&](Load& x, int h) {
+    auto copy = [&](int n) {
+      if (n < total) {
+        const int key = (w.w.blk.tile_lo + w.t) * kTile;
+        if (ct == 0)
+          meta[n & 7] = (key + kTile > w.w.blk.all_hi || key < w.w.blk.all_lo ? 1 : 0) |
+                        (w.t == w.first ? 2 : 0);
 #pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const int tok = key_next + p * C::kPassTokens + ptok;
-        x.k[p] = make_uint4(0, 0, 0, 0);
-        x.v[p] = x.k[p];
-        x.kp[p] = 0;
-        x.vp[p] = 0;
-        if (tok < hi_next) {
+        for (int p = 0; p < C::kPasses; ++p) {
+          const int tok = key + p * C::kPassTokens + ptok;
+          const bool have = tok < w.w.blk.hi;
+          int pg = pages[p];
+          if (have && (pg < 0 || pg >= a.num_pages)) atomicCAS(a.input_err, 0, 1);
+          if (pg < 0 || pg >= a.num_pages) pg = 0;
           const int off = tok & ((1 << a.lay.page_shift) - 1);
-          const uint8_t* rec = a.cache + (static_cast<long long>(pages[p]) * a.Hkv + h) * a.lay.record;
-          const uint8_t* c = rec + off * a.lay.code_row + part * 16;
-          const uint8_t* q = rec + a.lay.k_params + off * a.lay.param_row + group * 4;
-          x.k[p] = __ldg(reinterpret_cast<const uint4*>(c));
-          x.v[p] = __ldg(reinterpret_cast<const uint4*>(c + a.lay.v_codes));
-          x.kp[p] = __ldg(reinterpret_cast<const uint32_t*>(q));
-          x.vp[p] = __ldg(reinterpret_cast<const uint32_t*>(q + (a.lay.v_params - a.lay.k_params)));
+          const uint8_t* rec = a.cache + (static_cast<long long>(pg) * a.Hkv + w.w.h) * a.lay.record;
+          const uint8_t* c = rec + off * C::kCodeRow + part * 16;
+          const uint8_t* q = rec + a.lay.k_params + off * C::kParamRow + group * 4;
+          cp_async16(sb + C::kOffRing + ring16(n, p, 0), c, have);
+          cp_async16(sb + C::kOffRing + ring16(n, p, 1), c + a.lay.v_codes, have);
+          cp_async4(sb + C::kOffRing + ring4(n, p, 0), q, have);
+          cp_async4(sb + C::kOffRing + ring4(n, p, 1), q + (a.lay.v_params - a.lay.k_params), have);
         }
+        bool more = true;
+        if (++w.t >= w.last) more = w.next_item(a);
+        if (more) locate();
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto step = [&]() {  // w to its next tile
-      if (++w.t >= w.last) more = w.next_item(a);
-    };
-    // Largest params of a tile, numbers only: [parity][K, V][warp].
-    auto post_top = [&](const Load& x, int parity) {
+    // Largest params of tile n, numbers only: [parity][K, V][warp].
+    auto post_top = [&](int n) {
       uint32_t tk = 0, tv = 0;
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        if (!odd_param(x.kp[p])) tk = __vmaxu2(tk, x.kp[p] & 0x7fff7fffu);
-        if (!odd_param(x.vp[p])) tv = __vmaxu2(tv, x.vp[p] & 0x7fff7fffu);
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p, 0));
+        const uint32_t vp = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p, 1));
+        if (!odd_param(kp)) tk = __vmaxu2(tk, kp & 0x7fff7fffu);
+        if (!odd_param(vp)) tv = __vmaxu2(tv, vp & 0x7fff7fffu);
       }
       const uint32_t km = __reduce_max_sync(0xffffffffu, tk >> 16), ks = __reduce_max_sync(0xffffffffu, tk & 0xffffu);
       const uint32_t vm = __reduce_max_sync(0xffffffffu, tv >> 16), vs = __reduce_max_sync(0xffffffffu, tv & 0xffffu);
       if (lane == 0) {
-        top_param[parity][0][cw] = (km << 16) | ks;
-        top_param[parity][1][cw] = (vm << 16) | vs;
+        top_param[n & 1][0][cw] = (km << 16) | ks;
+        top_param[n & 1][1][cw] = (vm << 16) | vs;
       }
     };
     // |minimum| < 2^(e + 14), scale < 2^(e + 10)
-    auto unit_of = [&](int parity, int side) -> int {
+    auto unit_of = [&](int n, int side) -> int {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, top_param[parity][side][i]);
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, top_param[n & 1][side][i]);
       const int em = static_cast<int>(m >> 23), es = static_cast<int>((m >> 7) & 255);
       return max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
     };
+    // A word of codes is 16 bytes of the tile.  Threads two apart write to the
+    // same banks of neighbouring atoms: every other pair takes its words in
+    // another order.
+    const int flip = (part >> 1) & 1;
+    // Byte of the tile where word i of pass p goes (128-byte swizzle).
+    auto place = [&](int p, int i) -> int {
+      const int tok = p * C::kPassTokens + ptok;
+      const int chunk = part * 4 + (i ^ (flip << 1));
+      return (chunk >> 3) * C::kAtom + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
+    };
 
-    Load cur, nxt;
-    int h_next = w.w.h;
-    fetch_pages();
-    fetch_codes(cur, h_next);
-    int key0 = key_next;
-    int all_hi = w.w.blk.all_hi, all_lo = w.w.blk.all_lo;
-    bool first = true;   // the tile is its item's first
-    int v_run = 0;       // V's unit so far in the item
-    step();
-    bool nxt_ok = more;
-    if (nxt_ok) {
-      h_next = w.w.h;
-      fetch_pages();
-    }
-    post_top(cur, 0);
+    int v_run = 0;  // V's unit so far in the item
     bool ok = true;
-    for (int it = 0; it >= 0; ++it) {
-      const int st = it & 1, un = it & (kUnits - 1);
-      // The next tile's codes, and the pages of the one after it.
-      const int key_n = key_next;
-      int all_hi_n = 0, all_lo_n = 0;
-      bool first_n = false;
-      const bool have_next = nxt_ok;
-      if (have_next) {
-        first_n = w.t == w.first;
-        all_hi_n = w.w.blk.all_hi;
-        all_lo_n = w.w.blk.all_lo;
-        fetch_codes(nxt, h_next);
-        step();
-        nxt_ok = more;
-        if (nxt_ok) {
-          h_next = w.w.h;
-          fetch_pages();
-        }
-      }
+    locate();
+    for (int n = 0; n < C::kRing - 1; ++n) copy(n);
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
+    post_top(0);
+    for (int it = 0; it < total; ++it) {
+      const int ks = it % C::kKSt, vs = it % C::kVSt, un = it & (kUnits - 1);
+      copy(it + C::kRing - 1);
       // All four warps posted this tile's largest params (and, on the way, read
-      // the last tile's, so that those may be overwritten).
-      // Every warp passes here once a tile, so that one that gave up on a wait
-      // takes the others along.
-      ok = bar_and_128(2, ok);
+      // the last tile's, so that those may be overwritten).  Every warp passes
+      // here once a tile, so that one that gave up on a wait takes the others
+      // along.
+      ok = bar_and_128(C::kBlocks + 1, ok);
       if (!ok) break;
-      const int ke = unit_of(it & 1, 0);
-      v_run = first ? unit_of(it & 1, 1) : max(v_run, unit_of(it & 1, 1));
+      const int flags = meta[it & 7];
+      const int ke = unit_of(it, 0);
+      v_run = (flags & 2) ? unit_of(it, 1) : max(v_run, unit_of(it, 1));
       const int ve = v_run;
+      const bool edge = flags & 1;
       if (ct == 0) {
         k_unit[un] = pow2i(ke);
         v_exp[un] = ve;
         any_odd[un] = 0;
       }
       const float kd = pow2i(-ke), vd = pow2i(-ve);
-      const bool edge = key0 + kTile > all_hi || key0 < all_lo;
-      if (edge) asm volatile("bar.sync 2, 128;" ::: "memory");  // any_odd is 0
+      if (edge) asm volatile("bar.sync %0, 128;" ::"n"(C::kBlocks + 1) : "memory");  // any_odd is 0
 
-      if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar_kempty + 8u * st, ((it >> 1) & 1) ^ 1, ab))) {
+      if (it >= C::kKSt &&
+          !__all_sync(0xffffffffu, mbar_wait(bar_kempty + 8u * ks, ((it / C::kKSt) & 1) ^ 1, ab))) {
         ok = false;
-        if (!have_next) break;
         continue;
       }
-      // A word of codes is 16 bytes of the tile.  Threads two apart write to the
-      // same banks of neighbouring atoms: every other pair takes its words in
-      // another order.
-      const int flip = (part >> 1) & 1;
-      uint8_t* kt = smem + C::kOffK + st * C::kTileBytes;
+      uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        const int tok = p * C::kPassTokens + ptok;
-        const float s = param_scale(cur.kp[p]) * kd;
-        const float m = fmaf(8.f, s, param_min(cur.kp[p]) * kd);
+        const uint4 x = *reinterpret_cast<const uint4*>(ring + ring16(it, p, 0));
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p, 0));
+        const float s = param_scale(kp) * kd;
         const uint32_t s2 = pack_f16(s, s);
-        const uint32_t w0 = flip ? cur.k[p].z : cur.k[p].x, w1 = flip ? cur.k[p].w : cur.k[p].y;
-        const uint32_t w2 = flip ? cur.k[p].x : cur.k[p].z, w3 = flip ? cur.k[p].y : cur.k[p].w;
-        const uint32_t ww[4] = {w0, w1, w2, w3};
+        const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int chunk = part * 4 + (i ^ (flip << 1));
-          uint4 o;
-          o.x = mul_f16x2(codes_m8(ww[i], 0), s2);
-          o.y = mul_f16x2(codes_m8(ww[i], 1), s2);
-          o.z = mul_f16x2(codes_m8(ww[i], 2), s2);
-          o.w = mul_f16x2(codes_m8(ww[i], 3), s2);
-          *reinterpret_cast<uint4*>(kt + (chunk >> 3) * C::kAtom + tok * 128 +
-                                    (((chunk & 7) ^ (tok & 7)) << 4)) = o;
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(kt + place(p, i)) =
+              make_uint4(mul_f16x2(codes_m8(ww[i], 0), s2), mul_f16x2(codes_m8(ww[i], 1), s2),
+                         mul_f16x2(codes_m8(ww[i], 2), s2), mul_f16x2(codes_m8(ww[i], 3), s2));
         if (GROUP == 32 || (part & 1) == 0) {
+          const int tok = p * C::kPassTokens + ptok;
+          const float m = fmaf(8.f, s, param_min(kp) * kd);
           const __half h = __float2half_rn(m), l = __float2half_rn(m - __half2float(h));
           const __half slot[3] = {h, l, h};
-          uint8_t* ex = smem + C::kOffKEx + st * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
+          uint8_t* ex = smem + C::kOffKEx + ks * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
 #pragma unroll
           for (int e = 0; e < 3; ++e) {
             const int kk = 3 * group + e;
@@ -615,134 +644,156 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, GROUP>::kMinCtas)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_kfull + 8u * st);
+      if (lane == 0) mbar_arrive(bar_kfull + 8u * ks);
 
+      uint32_t vp[C::kPasses];
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) vp[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p, 1));
       if (edge) {
         // Values that are not numbers, where some row does not see them: left
         // out of the product; the rows that see them add them by themselves.
 #pragma unroll
         for (int p = 0; p < C::kPasses; ++p) {
           const int tok = p * C::kPassTokens + ptok;
-          const bool odd = odd_param(cur.vp[p]);
+          const bool odd = odd_param(vp[p]);
           // the token's threads are side by side in the warp
           uint32_t bits = odd ? 1u << group : 0u;
 #pragma unroll
           for (int d = 1; d < C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
           if (part == 0) odd_v[un][tok] = static_cast<uint8_t>(bits);
           if (bits) any_odd[un] = 1;
-          if (odd) cur.vp[p] = 0;
+          if (odd) vp[p] = 0;
         }
       }
-      if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar_vempty + 8u * st, ((it >> 1) & 1) ^ 1, ab))) {
+      if (it >= C::kVSt &&
+          !__all_sync(0xffffffffu, mbar_wait(bar_vempty + 8u * vs, ((it / C::kVSt) & 1) ^ 1, ab))) {
         ok = false;
-        if (!have_next) break;
         continue;
       }
-      uint8_t* vt = smem + C::kOffV + st * C::kTileBytes;
+      uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        const int tok = p * C::kPassTokens + ptok;
-        const float s = param_scale(cur.vp[p]) * vd;
-        const float m = fmaf(8.f, s, param_min(cur.vp[p]) * vd);
+        const uint4 x = *reinterpret_cast<const uint4*>(ring + ring16(it, p, 1));
+        const float s = param_scale(vp[p]) * vd;
+        const float m = fmaf(8.f, s, param_min(vp[p]) * vd);
         const uint32_t s2 = pack_f16(s, s), m2 = pack_f16(m, m);
-        const uint32_t w0 = flip ? cur.v[p].z : cur.v[p].x, w1 = flip ? cur.v[p].w : cur.v[p].y;
-        const uint32_t w2 = flip ? cur.v[p].x : cur.v[p].z, w3 = flip ? cur.v[p].y : cur.v[p].w;
-        const uint32_t ww[4] = {w0, w1, w2, w3};
+        const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int chunk = part * 4 + (i ^ (flip << 1));
-          uint4 o;
-          o.x = fma_f16x2(codes_m8(ww[i], 0), s2, m2);
-          o.y = fma_f16x2(codes_m8(ww[i], 1), s2, m2);
-          o.z = fma_f16x2(codes_m8(ww[i], 2), s2, m2);
-          o.w = fma_f16x2(codes_m8(ww[i], 3), s2, m2);
-          *reinterpret_cast<uint4*>(vt + (chunk >> 3) * C::kAtom + tok * 128 +
-                                    (((chunk & 7) ^ (tok & 7)) << 4)) = o;
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(vt + place(p, i)) =
+              make_uint4(fma_f16x2(codes_m8(ww[i], 0), s2, m2), fma_f16x2(codes_m8(ww[i], 1), s2, m2),
+                         fma_f16x2(codes_m8(ww[i], 2), s2, m2), fma_f16x2(codes_m8(ww[i], 3), s2, m2));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_vfull + 8u * st);
-      if (!have_next) break;
-      post_top(nxt, (it + 1) & 1);
-      cur = nxt;
-      key0 = key_n;
-      all_hi = all_hi_n;
-      all_lo = all_lo_n;
-      first = first_n;
+      if (lane == 0) mbar_arrive(bar_vfull + 8u * vs);
+      if (it + 1 < total) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
+        post_top(it + 1);
+      }
     }
-  } else if (lane == 0) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else {
+    regs_dec<C::kMmaRegs>();
+  }
+  if (warp == kMma && lane == 0) {
     // ---------------------------------------------------------- products
     constexpr uint32_t idS = idesc_f16(kRows, kTile, false);
     constexpr uint32_t idO = idesc_f16(kRows, HD, true);
     constexpr int kD = HD / 16, kC = kTile / 16;
-    uint64_t aQ[kD];
-    {
-      const uint64_t d0 = sdesc_sw128(sb + C::kOffQ, 16, 1024);
-#pragma unroll
-      for (int k = 0; k < kD; ++k) aQ[k] = sdesc_add(d0, (k >> 2) * C::kQAtom + (k & 3) * 32);
-    }
-    const uint64_t aX = sdesc_plain(sb + C::kOffQEx, 128, C::kExRow8);
     bool ok = true;
-    int it = 0, item = 0;
-    bool prev_first = false;  // was tile it - 1 its item's first?
-    auto issue_pv = [&](int jj, bool first) -> bool {
-      const int bb = jj & 1;
-      if (!mbar_wait(bar_pfull + 8u * bb, (jj >> 1) & 1, ab)) return false;
-      if (!mbar_wait(bar_vfull + 8u * bb, (jj >> 1) & 1, ab)) return false;
-      tc_fence_after();
-      uint64_t b[kC];
-      uint32_t p[kC];
-      const uint64_t d0 = sdesc_sw128(sb + C::kOffV + bb * C::kTileBytes, C::kAtom, 1024);
+    int tile = 0;                 // of the share
+    int it[C::kBlocks], item[C::kBlocks];  // tiles and items of a block of rows
 #pragma unroll
-      for (int k = 0; k < kC; ++k) {
-        b[k] = sdesc_add(d0, k * 2048);
-        p[k] = tmem + (bb ? 64u : 0u) + 8u * k;
+    for (int g = 0; g < C::kBlocks; ++g) it[g] = item[g] = 0;
+    bool prev_first = false;      // was the tile before its item's first?
+    int prev_blocks = 0;          // blocks of rows of its item
+    // P V of tile `tile - 1`.
+    auto issue_pv = [&]() -> bool {
+      const int vs = (tile - 1) % C::kVSt;
+      if (!mbar_wait(bar_vfull + 8u * vs, ((tile - 1) / C::kVSt) & 1, ab)) return false;
+      uint64_t b[kC];
+      const uint64_t d0 = sdesc_sw128(sb + C::kOffV + vs * C::kTileBytes, C::kAtom, 1024);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) b[k] = sdesc_add(d0, k * 2048);
+#pragma unroll
+      for (int g = 0; g < C::kBlocks; ++g) {
+        if (g >= prev_blocks) break;
+        const int jj = it[g] - 1, bb = jj & 1;
+        if (!mbar_wait(bar_pfull(g, bb), (jj >> 1) & 1, ab)) return false;
+        tc_fence_after();
+        uint32_t p[kC];
+#pragma unroll
+        for (int k = 0; k < kC; ++k) p[k] = tmem + 128u * g + (bb ? 64u : 0u) + 8u * k;
+        mma_ts_k(tmem + C::kColO + HD * g, p, b, idO, prev_first ? 0u : 1u);
+        mma_commit(bar_odone(g));
       }
-      mma_ts_k(tmem + C::kColO, p, b, idO, first ? 0u : 1u);
-      mma_commit(bar_odone);
-      mma_commit(bar_vempty + 8u * bb);
+      mma_commit(bar_vempty + 8u * vs);
       return true;
     };
     do {
       // The rows put an item's Q in place once they have read the O before, for
       // which the last product has to be issued first.
-      if (it > 0 && !issue_pv(it - 1, prev_first)) break;
-      if (!mbar_wait(bar_q, item & 1, ab)) break;
-      ++item;
-      for (; w.t < w.last; ++w.t, ++it) {
-        const int bb = it & 1;
-        // S over P of two tiles before: its product has to be complete.  (At an
-        // item's first tile the wait for Q has shown more than that, and the
-        // phase waited for here may be over already.)
-        if (it >= 2 && w.t > w.first && !mbar_wait(bar_odone, (it - 2) & 1, ab)) { ok = false; break; }
-        if (!mbar_wait(bar_kfull + 8u * bb, (it >> 1) & 1, ab)) { ok = false; break; }
-        tc_fence_after();
-        {
-          uint64_t b[kD];
-          const uint64_t d0 = sdesc_sw128(sb + C::kOffK + bb * C::kTileBytes, 16, 1024);
+      if (tile > 0 && !issue_pv()) break;
+      const int blocks = w.w.blk.rows > kRows ? C::kBlocks : 1;
 #pragma unroll
-          for (int k = 0; k < kD; ++k) b[k] = sdesc_add(d0, (k >> 2) * C::kAtom + (k & 3) * 32);
-          mma_ss_k(tmem + (bb ? 64u : 0u), aQ, b, idS, 0u);
-          const uint64_t x0 = sdesc_plain(sb + C::kOffKEx + bb * C::kKEx, 128, C::kExRow8);
+      for (int g = 0; g < C::kBlocks; ++g) {
+        if (g >= blocks) break;
+        ok = ok && mbar_wait(bar_q(g), item[g] & 1, ab);
+        ++item[g];
+      }
+      if (!ok) break;
+      for (; w.t < w.last; ++w.t) {
+        const int ks = tile % C::kKSt;
+        if (!mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab)) { ok = false; break; }
+        uint64_t b[kD];
+        const uint64_t d0 = sdesc_sw128(sb + C::kOffK + ks * C::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kD; ++k) b[k] = sdesc_add(d0, (k >> 2) * C::kAtom + (k & 3) * 32);
+        const uint64_t x0 = sdesc_plain(sb + C::kOffKEx + ks * C::kKEx, 128, C::kExRow8);
+#pragma unroll
+        for (int g = 0; g < C::kBlocks; ++g) {
+          if (g >= blocks) break;
+          const int bb = it[g] & 1;
+          // S over P of two tiles before: its product has to be complete.  (At
+          // an item's first tile the wait for Q has shown more than that, and
+          // the phase waited for here may be over already.)
+          if (it[g] >= 2 && w.t > w.first && !mbar_wait(bar_odone(g), (it[g] - 2) & 1, ab)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint64_t q[kD];
+          const uint64_t q0 = sdesc_sw128(sb + C::kOffQ + g * C::kQTile, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kD; ++k) q[k] = sdesc_add(q0, (k >> 2) * C::kQAtom + (k & 3) * 32);
+          const uint32_t dst = tmem + 128u * g + (bb ? 64u : 0u);
+          mma_ss_k(dst, q, b, idS, 0u);
+          const uint64_t qx = sdesc_plain(sb + C::kOffQEx + g * C::kQEx, 128, C::kExRow8);
 #pragma unroll
           for (int k = 0; k < C::kExSteps; ++k)
-            mma_ss(tmem + (bb ? 64u : 0u), sdesc_add(aX, k * 256), sdesc_add(x0, k * 256), idS, 1u);
+            mma_ss(dst, sdesc_add(qx, k * 256), sdesc_add(x0, k * 256), idS, 1u);
+          mma_commit(bar_sfull(g, bb));
         }
-        mma_commit(bar_sfull + 8u * bb);
-        mma_commit(bar_kempty + 8u * bb);
-        if (w.t > w.first && !issue_pv(it - 1, w.t - 1 == w.first)) { ok = false; break; }
+        if (!ok) break;
+        mma_commit(bar_kempty + 8u * ks);
+        if (w.t > w.first && !issue_pv()) { ok = false; break; }
+#pragma unroll
+        for (int g = 0; g < C::kBlocks; ++g)
+          if (g < blocks) ++it[g];
+        ++tile;
+        prev_first = w.t == w.first;
+        prev_blocks = blocks;
       }
-      prev_first = w.last - 1 == w.first;
     } while (ok && w.next_item(a));
-    if (ok && it > 0 && *abort_flag == 0) issue_pv(it - 1, prev_first);
+    if (ok && tile > 0 && *abort_flag == 0) issue_pv();
     mma_commit(bar_drain);
     mbar_wait_drain(bar_drain, 0);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -763,8 +814,8 @@ cudaError_t launch_chunk(const Kv4AttnArgs& a, cudaStream_t stream, int* ctas) {
   }
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
-  *ctas = C::kMinCtas * sms < kKv4MaxChunkCtas ? C::kMinCtas * sms : kKv4MaxChunkCtas;
-  kv4_chunk_kernel<HD, GROUP><<<*ctas, kThreads, C::kSmem, stream>>>(a);
+  *ctas = sms < kKv4MaxChunkCtas ? sms : kKv4MaxChunkCtas;
+  kv4_chunk_kernel<HD, GROUP><<<*ctas, C::kThreads, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -187,12 +187,12 @@ struct Kv4Walk {
 
 // The record a CTA leaves for the merge: the item, cut by this share's end,
 // that begins in it (x: first query of its request, y: first row of its block,
-// z: rows + 256 * K/V head, 0: there is none, w: the last CTA with a part of
+// z: rows + 512 * K/V head, 0: there is none, w: the last CTA with a part of
 // it).  Partial results of CTA i are number 2 i (of its first item, begun
 // before) and 2 i + 1 (of its last, begun here).
 template <int kTile>
 __device__ __forceinline__ int4 kv4_split_record(const Kv4Walk<kTile>& w, const Kv4Share& s) {
-  return make_int4(w.req.start, w.blk.row0, w.blk.rows + 256 * w.h,
+  return make_int4(w.req.start, w.blk.row0, w.blk.rows + 512 * w.h,
                    static_cast<int>((w.item + w.blk.units - 1) / s.per));
 }
 
