@@ -6,12 +6,16 @@
 // (kv4_sched.cuh).  Both products run on the tensor cores out of tensor memory as
 // in the bf16 forward (S double buffered, P over S as the A operand of P V, O
 // resident); what differs is where K and V come from:
-//   - the converter, four warps, copies a tile's codes and params some tiles
-//     ahead (cp.async; a thread's own 16 bytes, so nobody waits for anybody) and
-//     writes them as fp16 tiles in the 128-byte-swizzled layout the products take;
+//   - two converters, four warps each for K and for V, copy a tile's codes and
+//     params some tiles ahead (cp.async; a thread's own 16 bytes, so nobody waits
+//     for anybody) and write them as fp16 tiles in the 128-byte-swizzled layout
+//     the products take;
 //   - a warpgroup for each 128 rows (thread = row = TMEM lane) loads Q, does the
 //     softmax and writes O; the two share every converted tile;
-//   - one thread issues the products.
+//   - one thread for each 128 rows issues the products.
+// Two issuers and two converters because one of either was what a tile waited
+// for: a thread's chain of dependent instructions, not the pipes (one of each:
+// 3890 clocks a tile, of which the issuer worked 3040 and the converter 2480).
 //
 // K.  (code - 8) * scale has at most 8 + 3 significant bits and so is exact in
 // fp16, as Q is (8 bits) after a scaling of each row by a power of two.  The
@@ -111,7 +115,7 @@ struct Cfg {
   static constexpr int kAtoms = HD / 64;
   static constexpr int kBlocks = HD == 256 ? 1 : 2;      // warpgroups of rows
   static constexpr int kBlockRows = kBlocks * kRows;
-  static constexpr int kThreads = 128 * (kBlocks + 2);   // + converter, products
+  static constexpr int kThreads = 128 * (kBlocks + 3);   // + converters of K and V, products
   static constexpr int kQAtom = kRows * 128, kQTile = kAtoms * kQAtom;
   static constexpr int kAtom = kTile * 128, kTileBytes = kAtoms * kAtom;  // K or V tile
   static constexpr int kKSt = HD == 256 ? 1 : 2, kVSt = 2;
@@ -120,21 +124,20 @@ struct Cfg {
   static constexpr int kExRow8 = kExSteps * 256;  // bytes of eight rows
   static constexpr int kQEx = kRows / 8 * kExRow8, kKEx = kTile / 8 * kExRow8;
   // Converter: threads a token's row of codes, tokens a pass, passes a tile;
-  // tiles of codes in flight or in use, each thread's own 16 + 16 + 4 + 4 bytes
-  // a pass.
+  // tiles of codes in flight or in use, each thread's own 16 + 4 bytes a pass.
   static constexpr int kTpr = HD / 32, kPassTokens = 128 / kTpr, kPasses = kTile / kPassTokens;
   static constexpr int kRing = HD == 256 ? 2 : 4;
-  static constexpr int kRingTile = kPasses * 128 * 40;
+  static constexpr int kRingTile = kPasses * 128 * 20;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kBlocks * kQTile;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
   static constexpr int kOffQEx = kOffV + kVSt * kTileBytes;
   static constexpr int kOffKEx = kOffQEx + kBlocks * kQEx;
   static constexpr int kOffRing = kOffKEx + kKSt * kKEx;
-  static constexpr int kOffBar = kOffRing + kRing * kRingTile;
-  // k_full[2], k_empty[2], v_full[2], v_empty[2], drain, then for each block of
-  // rows q_full, s_full[2], p_full[2], o_done
-  static constexpr int kNumBar = 9 + 6 * kBlocks;
+  static constexpr int kOffBar = kOffRing + 2 * kRing * kRingTile;
+  // k_full[2], k_empty[2], v_full[2], v_empty[2], then for each block of rows
+  // q_full, s_full[2], p_full[2], o_done, drain
+  static constexpr int kNumBar = 8 + 7 * kBlocks;
   static constexpr int kOffMisc = kOffBar + kNumBar * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 230000, "shared memory budget");
@@ -142,13 +145,13 @@ struct Cfg {
   static constexpr uint32_t kColO = 128 * kBlocks;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kColO + kBlocks * HD <= kTmemCols, "tensor memory budget");
-  // Registers a thread of the warpgroups (rows, converter, products) out of the
-  // launch's.
-  static constexpr int kLaunchRegs = kBlocks == 2 ? 128 : 168;
-  static constexpr int kRowRegs = kBlocks == 2 ? 152 : 200;
-  static constexpr int kConvRegs = kBlocks == 2 ? 112 : 168;
-  static constexpr int kMmaRegs = kBlocks == 2 ? 96 : 128;
-  static_assert(kBlocks * kRowRegs + kConvRegs + kMmaRegs <= (kBlocks + 2) * kLaunchRegs, "register split");
+  // Registers a thread of the warpgroups (rows, each converter, products) out
+  // of the launch's.
+  static constexpr int kLaunchRegs = kBlocks == 2 ? 96 : 128;
+  static constexpr int kRowRegs = kBlocks == 2 ? 144 : 208;
+  static constexpr int kConvRegs = kBlocks == 2 ? 64 : 104;
+  static constexpr int kMmaRegs = kBlocks == 2 ? 64 : 96;
+  static_assert(kBlocks * kRowRegs + 2 * kConvRegs + kMmaRegs <= (kBlocks + 3) * kLaunchRegs, "register split");
 };
 
 __device__ __forceinline__ bool bar_and_128(int id, bool pred) {
@@ -200,18 +203,203 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ha
                : "memory");
 }
 
+// What the converters leave for the rows, by tile (a ring of kUnits).
+struct Units {
+  float k_unit[kUnits];          // 2^kexp
+  int v_exp[kUnits];
+  int any_odd[kUnits];
+  uint8_t odd_v[kUnits][kTile];  // groups of a token's V that are not numbers
+  uint32_t top_param[2][2][4];   // [side][tile parity][warp]
+  int meta[2][8];                // of a converter's tiles: bit 0 edge, bit 1 item's first
+};
+
+// The converter of K (kSide 0) or V (1): four warps; `w` is its own walk.
+template <int HD, int GROUP, int kSide>
+__device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROUP>::kBlockRows>& w,
+                                        uint8_t* smem, uint32_t sb, uint32_t bar_full,
+                                        uint32_t bar_empty, Units& un, const Abort& ab) {
+  using C = Cfg<HD, GROUP>;
+  constexpr int kSt = kSide ? C::kVSt : C::kKSt;
+  constexpr int kBar = C::kBlocks + 1 + kSide;  // named barrier of these four warps
+  const int ct = threadIdx.x & 127, cw = ct >> 5, lane = ct & 31;
+  const int part = ct % C::kTpr;   // 32-channel block
+  const int ptok = ct / C::kTpr;   // token of a pass
+  const int group = part * 32 / GROUP;
+  const int total = static_cast<int>(w.u_end - w.u);
+  const int codes_at = kSide ? a.lay.v_codes : 0, params_at = kSide ? a.lay.v_params : a.lay.k_params;
+  // This thread's place in the ring: codes of pass p of tile n, then params.
+  uint8_t* ring = smem + C::kOffRing + kSide * C::kRing * C::kRingTile;
+  const uint32_t ring_u32 = sb + C::kOffRing + kSide * C::kRing * C::kRingTile;
+  auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + ct * 16; };
+  auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + 2048 + ct * 4; };
+  int pages[C::kPasses];  // of the tile w stands at, the next to be copied
+  auto locate = [&]() {
+    const int key = (w.w.blk.tile_lo + w.t) * kTile;
+#pragma unroll
+    for (int p = 0; p < C::kPasses; ++p) {
+      const int tok = key + p * C::kPassTokens + ptok;
+      pages[p] = -1;
+      if (tok < w.w.blk.hi)
+        pages[p] = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages +
+                         (tok >> a.lay.page_shift));
+    }
+  };
+  auto copy = [&](int n) {
+    if (n < total) {
+      const int key = (w.w.blk.tile_lo + w.t) * kTile;
+      if (ct == 0)
+        un.meta[kSide][n & 7] = (key + kTile > w.w.blk.all_hi || key < w.w.blk.all_lo ? 1 : 0) |
+                                (w.t == w.first ? 2 : 0);
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const int tok = key + p * C::kPassTokens + ptok;
+        const bool have = tok < w.w.blk.hi;
+        int pg = pages[p];
+        if (pg < 0 || pg >= a.num_pages) {
+          if (have) atomicCAS(a.input_err, 0, 1);
+          pg = 0;
+        }
+        const int off = tok & ((1 << a.lay.page_shift) - 1);
+        const uint8_t* rec = a.cache + (static_cast<long long>(pg) * a.Hkv + w.w.h) * a.lay.record;
+        cp_async16(ring_u32 + ring16(n, p), rec + codes_at + off * C::kCodeRow + part * 16, have);
+        cp_async4(ring_u32 + ring4(n, p), rec + params_at + off * C::kParamRow + group * 4, have);
+      }
+      bool more = true;
+      if (++w.t >= w.last) more = w.next_item(a);
+      if (more) locate();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // Largest params of tile n, numbers only.
+  auto post_top = [&](int n) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < C::kPasses; ++p) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p));
+      if (!odd_param(x)) top = __vmaxu2(top, x & 0x7fff7fffu);
+    }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top >> 16), sc = __reduce_max_sync(0xffffffffu, top & 0xffffu);
+    if (lane == 0) un.top_param[kSide][n & 1][cw] = (m << 16) | sc;
+  };
+  // |minimum| < 2^(e + 14), scale < 2^(e + 10)
+  auto unit_of = [&](int n) -> int {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, un.top_param[kSide][n & 1][i]);
+    const int em = static_cast<int>(m >> 23), es = static_cast<int>((m >> 7) & 255);
+    return max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
+  };
+  // A word of codes is 16 bytes of the tile.  Threads two apart write to the
+  // same banks of neighbouring atoms: every other pair takes its words in
+  // another order.
+  const int flip = (part >> 1) & 1;
+  int place[4];  // byte of the tile where word i of pass 0 goes (128-byte swizzle)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int chunk = part * 4 + (i ^ (flip << 1));
+    place[i] = (chunk >> 3) * C::kAtom + ptok * 128 + (((chunk & 7) ^ (ptok & 7)) << 4);
+  }
+  static_assert(C::kPassTokens % 8 == 0, "a pass later the swizzle is the same");
+
+  int e_run = 0;  // V's unit so far in the item
+  bool ok = true;
+  locate();
+  for (int n = 0; n < C::kRing - 1; ++n) copy(n);
+  asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
+  post_top(0);
+  for (int it = 0; it < total; ++it) {
+    const int st = it % kSt, slot = it & (kUnits - 1);
+    copy(it + C::kRing - 1);
+    // All four warps posted this tile's largest params (and, on the way, read
+    // the last tile's, so that those may be overwritten).  Every warp passes
+    // here once a tile, so that one that gave up on a wait takes the others
+    // along.
+    ok = bar_and_128(kBar, ok);
+    if (!ok) break;
+    const int flags = un.meta[kSide][it & 7];
+    // K's unit is the tile's own; V's grows only, within an item.
+    e_run = kSide == 0 || (flags & 2) ? unit_of(it) : max(e_run, unit_of(it));
+    const float unit = pow2i(-e_run);
+    if (ct == 0) {
+      if (kSide == 0) {
+        un.k_unit[slot] = pow2i(e_run);
+      } else {
+        un.v_exp[slot] = e_run;
+        un.any_odd[slot] = 0;
+      }
+    }
+    uint32_t par[C::kPasses];
+#pragma unroll
+    for (int p = 0; p < C::kPasses; ++p) par[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p));
+    if (kSide == 1 && (flags & 1)) {
+      // Values that are not numbers, where some row does not see them: left out
+      // of the product; the rows that see them add them by themselves.
+      asm volatile("bar.sync %0, 128;" ::"n"(kBar) : "memory");  // any_odd is 0
+#pragma unroll
+      for (int p = 0; p < C::kPasses; ++p) {
+        const bool odd = odd_param(par[p]);
+        // the token's threads are side by side in the warp
+        uint32_t bits = odd ? 1u << group : 0u;
+#pragma unroll
+        for (int d = 1; d < C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
+        if (part == 0) un.odd_v[slot][p * C::kPassTokens + ptok] = static_cast<uint8_t>(bits);
+        if (bits) un.any_odd[slot] = 1;
+        if (odd) par[p] = 0;
+      }
+    }
+    if (it >= kSt && !__all_sync(0xffffffffu, mbar_wait(bar_empty + 8u * st, ((it / kSt) & 1) ^ 1, ab))) {
+      ok = false;
+      continue;
+    }
+    uint8_t* tile = smem + (kSide ? C::kOffV : C::kOffK) + st * C::kTileBytes;
+#pragma unroll
+    for (int p = 0; p < C::kPasses; ++p) {
+      const uint4 x = *reinterpret_cast<const uint4*>(ring + ring16(it, p));
+      const float s = param_scale(par[p]) * unit;
+      const float m = fmaf(8.f, s, param_min(par[p]) * unit);
+      const uint32_t s2 = pack_f16(s, s), m2 = pack_f16(m, m);
+      const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t c = codes_m8(ww[i], e);
+          o[e] = kSide ? fma_f16x2(c, s2, m2) : mul_f16x2(c, s2);
+        }
+        *reinterpret_cast<uint4*>(tile + place[i] + p * C::kPassTokens * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (kSide == 0 && (GROUP == 32 || (part & 1) == 0)) {
+        const int tok = p * C::kPassTokens + ptok;
+        const __half h = __float2half_rn(m), l = __float2half_rn(m - __half2float(h));
+        const __half part3[3] = {h, l, h};
+        uint8_t* ex = smem + C::kOffKEx + st * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const int kk = 3 * group + e;
+          *reinterpret_cast<__half*>(ex + (kk >> 3) * 128 + (kk & 7) * 2) = part3[e];
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_full + 8u * st);
+    if (it + 1 < total) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
+      post_top(it + 1);
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 template <int HD, int GROUP>
 __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a) {
   using C = Cfg<HD, GROUP>;
-  constexpr int kThreads = C::kThreads, kConv = 4 * C::kBlocks, kMma = kConv + 4;  // first warps
+  constexpr int kThreads = C::kThreads;
+  constexpr int kConvK = 4 * C::kBlocks, kConvV = kConvK + 4, kMma = kConvV + 4;  // first warps
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kThreads / 32 + 2];
-  __shared__ float k_unit[kUnits];         // 2^kexp of a tile
-  __shared__ int v_exp[kUnits];
-  __shared__ uint32_t top_param[2][2][4];  // [tile parity][K, V][warp]
-  __shared__ uint8_t odd_v[kUnits][kTile]; // groups of a token's V that are not numbers
-  __shared__ int any_odd[kUnits];
-  __shared__ int meta[8];                  // of the converter's tiles: bit 0 edge, bit 1 item's first
+  __shared__ Units un;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t pad = ((raw_u32 + 1023u) & ~1023u) - raw_u32;
@@ -219,11 +407,12 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   const uint32_t sb = raw_u32 + pad;
   const uint32_t bar0 = sb + C::kOffBar;
   const uint32_t bar_kfull = bar0, bar_kempty = bar0 + 16, bar_vfull = bar0 + 32,
-                 bar_vempty = bar0 + 48, bar_drain = bar0 + 64;
-  auto bar_q = [&](int g) { return bar0 + 72u + 48u * g; };
-  auto bar_sfull = [&](int g, int b) { return bar0 + 80u + 48u * g + 8u * b; };
-  auto bar_pfull = [&](int g, int b) { return bar0 + 96u + 48u * g + 8u * b; };
-  auto bar_odone = [&](int g) { return bar0 + 112u + 48u * g; };
+                 bar_vempty = bar0 + 48;
+  auto bar_q = [&](int g) { return bar0 + 64u + 56u * g; };
+  auto bar_sfull = [&](int g, int b) { return bar0 + 72u + 56u * g + 8u * b; };
+  auto bar_pfull = [&](int g, int b) { return bar0 + 88u + 56u * g + 8u * b; };
+  auto bar_odone = [&](int g) { return bar0 + 104u + 56u * g; };
+  auto bar_drain = [&](int g) { return bar0 + 112u + 56u * g; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -237,11 +426,10 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_kfull + 8 * s, 4);
-      mbar_init(bar_kempty + 8 * s, 1);
+      mbar_init(bar_kempty + 8 * s, C::kBlocks);
       mbar_init(bar_vfull + 8 * s, 4);
-      mbar_init(bar_vempty + 8 * s, 1);
+      mbar_init(bar_vempty + 8 * s, C::kBlocks);
     }
-    mbar_init(bar_drain, 1);
     for (int g = 0; g < C::kBlocks; ++g) {
       mbar_init(bar_q(g), 4);
       for (int b = 0; b < 2; ++b) {
@@ -249,6 +437,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
         mbar_init(bar_pfull(g, b), 4);
       }
       mbar_init(bar_odone(g), 1);
+      mbar_init(bar_drain(g), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -269,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   Tiles<C::kBlockRows> w;
   w.begin(a, share);
 
-  if (warp < kConv) {
+  if (warp < kConvK) {
     // ---------------------------------------------------------- rows
     regs_inc<C::kRowRegs>();
     const int g = warp >> 2;                 // block of 128 rows
@@ -355,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       int v_ref = 0;
       uint32_t nan_groups = 0;
       for (; w.t < w.last; ++w.t, ++it, ++tile) {
-        const int bb = it & 1, un = tile & (kUnits - 1);
+        const int bb = it & 1, slot = tile & (kUnits - 1);
         const uint32_t scol = tl + (bb ? 64u : 0u);
         const int key0 = (k.blk.tile_lo + w.t) * kTile;
         if (!__all_sync(0xffffffffu, mbar_wait(bar_sfull(g, bb), (it >> 1) & 1, ab))) {
@@ -366,8 +555,8 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
         uint32_t sr[2][32];
         tmem_ld32(scol, sr[0]);
         tmem_ld32(scol + 32, sr[1]);
-        const float mult = row_scale * k_unit[un];
-        const int ve = v_exp[un];
+        const float mult = row_scale * un.k_unit[slot];
+        const int ve = un.v_exp[slot];
         tmem_wait_ld();
         const bool edge = key0 + kTile > k.blk.all_hi || key0 < k.blk.all_lo;
         if (edge) {
@@ -378,9 +567,9 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
               sr[c][e] = static_cast<uint32_t>(key0 + 32 * c + e - row_lo) < seen
                              ? sr[c][e]
                              : __float_as_uint(-INFINITY);
-          if (any_odd[un])
+          if (un.any_odd[slot])
             for (int e = 0; e < kTile; ++e)
-              if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= odd_v[un][e];
+              if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= un.odd_v[slot][e];
         }
         float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -490,305 +679,101 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       first_item = false;
     } while (w.next_item(a));
     if (tid == 0) a.split[blockIdx.x] = record;
+  } else if (warp < kConvV) {
+    regs_dec<C::kConvRegs>();
+    convert<HD, GROUP, 0>(a, w, smem, sb, bar_kfull, bar_kempty, un, ab);
   } else if (warp < kMma) {
-    // ---------------------------------------------------------- codes to tiles
-    if constexpr (C::kConvRegs < C::kLaunchRegs) regs_dec<C::kConvRegs>();
-    const int ct = tid - 32 * kConv, cw = warp - kConv;
-    const int part = ct % C::kTpr;   // 32-channel block
-    const int ptok = ct / C::kTpr;   // token of a pass
-    const int group = part * 32 / GROUP;
-    const int total = static_cast<int>(w.u_end - w.u);
-    // This thread's place in the ring: K codes, V codes, K params, V params of
-    // pass p of tile n at ring16(n, p), + 2048, ...
-    uint8_t* ring = smem + C::kOffRing;
-    auto ring16 = [&](int n, int p, int side) {
-      return (n % C::kRing) * C::kRingTile + p * 128 * 40 + side * 2048 + ct * 16;
-    };
-    auto ring4 = [&](int n, int p, int side) {
-      return (n % C::kRing) * C::kRingTile + p * 128 * 40 + 4096 + side * 512 + ct * 4;
-    };
-    int pages[C::kPasses];  // of the tile w stands at, the next to be copied
-    auto locate = [&]() {
-      const int key = (w.w.blk.tile_lo + w.t) * kTile;
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const int tok = key + p * C::kPassTokens + ptok;
-        pages[p] = -1;
-        if (tok < w.w.blk.hi)
-          pages[p] = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages +
-                           (tok >> a.lay.page_shift));
-      }
-    };
-    auto copy = [&](int n) {
-      if (n < total) {
-        const int key = (w.w.blk.tile_lo + w.t) * kTile;
-        if (ct == 0)
-          meta[n & 7] = (key + kTile > w.w.blk.all_hi || key < w.w.blk.all_lo ? 1 : 0) |
-                        (w.t == w.first ? 2 : 0);
-#pragma unroll
-        for (int p = 0; p < C::kPasses; ++p) {
-          const int tok = key + p * C::kPassTokens + ptok;
-          const bool have = tok < w.w.blk.hi;
-          int pg = pages[p];
-          if (have && (pg < 0 || pg >= a.num_pages)) atomicCAS(a.input_err, 0, 1);
-          if (pg < 0 || pg >= a.num_pages) pg = 0;
-          const int off = tok & ((1 << a.lay.page_shift) - 1);
-          const uint8_t* rec = a.cache + (static_cast<long long>(pg) * a.Hkv + w.w.h) * a.lay.record;
-          const uint8_t* c = rec + off * C::kCodeRow + part * 16;
-          const uint8_t* q = rec + a.lay.k_params + off * C::kParamRow + group * 4;
-          cp_async16(sb + C::kOffRing + ring16(n, p, 0), c, have);
-          cp_async16(sb + C::kOffRing + ring16(n, p, 1), c + a.lay.v_codes, have);
-          cp_async4(sb + C::kOffRing + ring4(n, p, 0), q, have);
-          cp_async4(sb + C::kOffRing + ring4(n, p, 1), q + (a.lay.v_params - a.lay.k_params), have);
-        }
-        bool more = true;
-        if (++w.t >= w.last) more = w.next_item(a);
-        if (more) locate();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    // Largest params of tile n, numbers only: [parity][K, V][warp].
-    auto post_top = [&](int n) {
-      uint32_t tk = 0, tv = 0;
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p, 0));
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p, 1));
-        if (!odd_param(kp)) tk = __vmaxu2(tk, kp & 0x7fff7fffu);
-        if (!odd_param(vp)) tv = __vmaxu2(tv, vp & 0x7fff7fffu);
-      }
-      const uint32_t km = __reduce_max_sync(0xffffffffu, tk >> 16), ks = __reduce_max_sync(0xffffffffu, tk & 0xffffu);
-      const uint32_t vm = __reduce_max_sync(0xffffffffu, tv >> 16), vs = __reduce_max_sync(0xffffffffu, tv & 0xffffu);
-      if (lane == 0) {
-        top_param[n & 1][0][cw] = (km << 16) | ks;
-        top_param[n & 1][1][cw] = (vm << 16) | vs;
-      }
-    };
-    // |minimum| < 2^(e + 14), scale < 2^(e + 10)
-    auto unit_of = [&](int n, int side) -> int {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, top_param[n & 1][side][i]);
-      const int em = static_cast<int>(m >> 23), es = static_cast<int>((m >> 7) & 255);
-      return max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
-    };
-    // A word of codes is 16 bytes of the tile.  Threads two apart write to the
-    // same banks of neighbouring atoms: every other pair takes its words in
-    // another order.
-    const int flip = (part >> 1) & 1;
-    // Byte of the tile where word i of pass p goes (128-byte swizzle).
-    auto place = [&](int p, int i) -> int {
-      const int tok = p * C::kPassTokens + ptok;
-      const int chunk = part * 4 + (i ^ (flip << 1));
-      return (chunk >> 3) * C::kAtom + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
-    };
-
-    int v_run = 0;  // V's unit so far in the item
-    bool ok = true;
-    locate();
-    for (int n = 0; n < C::kRing - 1; ++n) copy(n);
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
-    post_top(0);
-    for (int it = 0; it < total; ++it) {
-      const int ks = it % C::kKSt, vs = it % C::kVSt, un = it & (kUnits - 1);
-      copy(it + C::kRing - 1);
-      // All four warps posted this tile's largest params (and, on the way, read
-      // the last tile's, so that those may be overwritten).  Every warp passes
-      // here once a tile, so that one that gave up on a wait takes the others
-      // along.
-      ok = bar_and_128(C::kBlocks + 1, ok);
-      if (!ok) break;
-      const int flags = meta[it & 7];
-      const int ke = unit_of(it, 0);
-      v_run = (flags & 2) ? unit_of(it, 1) : max(v_run, unit_of(it, 1));
-      const int ve = v_run;
-      const bool edge = flags & 1;
-      if (ct == 0) {
-        k_unit[un] = pow2i(ke);
-        v_exp[un] = ve;
-        any_odd[un] = 0;
-      }
-      const float kd = pow2i(-ke), vd = pow2i(-ve);
-      if (edge) asm volatile("bar.sync %0, 128;" ::"n"(C::kBlocks + 1) : "memory");  // any_odd is 0
-
-      if (it >= C::kKSt &&
-          !__all_sync(0xffffffffu, mbar_wait(bar_kempty + 8u * ks, ((it / C::kKSt) & 1) ^ 1, ab))) {
-        ok = false;
-        continue;
-      }
-      uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const uint4 x = *reinterpret_cast<const uint4*>(ring + ring16(it, p, 0));
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p, 0));
-        const float s = param_scale(kp) * kd;
-        const uint32_t s2 = pack_f16(s, s);
-        const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(kt + place(p, i)) =
-              make_uint4(mul_f16x2(codes_m8(ww[i], 0), s2), mul_f16x2(codes_m8(ww[i], 1), s2),
-                         mul_f16x2(codes_m8(ww[i], 2), s2), mul_f16x2(codes_m8(ww[i], 3), s2));
-        if (GROUP == 32 || (part & 1) == 0) {
-          const int tok = p * C::kPassTokens + ptok;
-          const float m = fmaf(8.f, s, param_min(kp) * kd);
-          const __half h = __float2half_rn(m), l = __float2half_rn(m - __half2float(h));
-          const __half slot[3] = {h, l, h};
-          uint8_t* ex = smem + C::kOffKEx + ks * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
-#pragma unroll
-          for (int e = 0; e < 3; ++e) {
-            const int kk = 3 * group + e;
-            *reinterpret_cast<__half*>(ex + (kk >> 3) * 128 + (kk & 7) * 2) = slot[e];
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_kfull + 8u * ks);
-
-      uint32_t vp[C::kPasses];
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) vp[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p, 1));
-      if (edge) {
-        // Values that are not numbers, where some row does not see them: left
-        // out of the product; the rows that see them add them by themselves.
-#pragma unroll
-        for (int p = 0; p < C::kPasses; ++p) {
-          const int tok = p * C::kPassTokens + ptok;
-          const bool odd = odd_param(vp[p]);
-          // the token's threads are side by side in the warp
-          uint32_t bits = odd ? 1u << group : 0u;
-#pragma unroll
-          for (int d = 1; d < C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
-          if (part == 0) odd_v[un][tok] = static_cast<uint8_t>(bits);
-          if (bits) any_odd[un] = 1;
-          if (odd) vp[p] = 0;
-        }
-      }
-      if (it >= C::kVSt &&
-          !__all_sync(0xffffffffu, mbar_wait(bar_vempty + 8u * vs, ((it / C::kVSt) & 1) ^ 1, ab))) {
-        ok = false;
-        continue;
-      }
-      uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-#pragma unroll
-      for (int p = 0; p < C::kPasses; ++p) {
-        const uint4 x = *reinterpret_cast<const uint4*>(ring + ring16(it, p, 1));
-        const float s = param_scale(vp[p]) * vd;
-        const float m = fmaf(8.f, s, param_min(vp[p]) * vd);
-        const uint32_t s2 = pack_f16(s, s), m2 = pack_f16(m, m);
-        const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(vt + place(p, i)) =
-              make_uint4(fma_f16x2(codes_m8(ww[i], 0), s2, m2), fma_f16x2(codes_m8(ww[i], 1), s2, m2),
-                         fma_f16x2(codes_m8(ww[i], 2), s2, m2), fma_f16x2(codes_m8(ww[i], 3), s2, m2));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_vfull + 8u * vs);
-      if (it + 1 < total) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
-        post_top(it + 1);
-      }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    regs_dec<C::kConvRegs>();
+    convert<HD, GROUP, 1>(a, w, smem, sb, bar_vfull, bar_vempty, un, ab);
   } else {
     regs_dec<C::kMmaRegs>();
   }
-  if (warp == kMma && lane == 0) {
+  if (warp >= kMma && warp < kMma + C::kBlocks && lane == 0) {
     // ---------------------------------------------------------- products
     constexpr uint32_t idS = idesc_f16(kRows, kTile, false);
     constexpr uint32_t idO = idesc_f16(kRows, HD, true);
     constexpr int kD = HD / 16, kC = kTile / 16;
+    const int g = warp - kMma;    // block of rows
     bool ok = true;
     int tile = 0;                 // of the share
-    int it[C::kBlocks], item[C::kBlocks];  // tiles and items of a block of rows
-#pragma unroll
-    for (int g = 0; g < C::kBlocks; ++g) it[g] = item[g] = 0;
-    bool prev_first = false;      // was the tile before its item's first?
-    int prev_blocks = 0;          // blocks of rows of its item
-    // P V of tile `tile - 1`.
+    int it = 0, item = 0;         // tiles and items of this block of rows
+    bool prev_first = false;      // was its last tile its item's first?
+    uint64_t q0, qx;              // this block's Q
+    q0 = sdesc_sw128(sb + C::kOffQ + g * C::kQTile, 16, 1024);
+    qx = sdesc_plain(sb + C::kOffQEx + g * C::kQEx, 128, C::kExRow8);
+    const uint64_t k0 = sdesc_sw128(sb + C::kOffK, 16, 1024);
+    const uint64_t kx = sdesc_plain(sb + C::kOffKEx, 128, C::kExRow8);
+    const uint64_t v0 = sdesc_sw128(sb + C::kOffV, C::kAtom, 1024);
+    const uint32_t ts = tmem + 128u * g, to = tmem + C::kColO + HD * g;
+    // P V of tile `tile - 1`, this block's `it - 1`.
     auto issue_pv = [&]() -> bool {
-      const int vs = (tile - 1) % C::kVSt;
+      const int vs = (tile - 1) % C::kVSt, bb = (it - 1) & 1;
       if (!mbar_wait(bar_vfull + 8u * vs, ((tile - 1) / C::kVSt) & 1, ab)) return false;
+      if (!mbar_wait(bar_pfull(g, bb), ((it - 1) >> 1) & 1, ab)) return false;
+      tc_fence_after();
       uint64_t b[kC];
-      const uint64_t d0 = sdesc_sw128(sb + C::kOffV + vs * C::kTileBytes, C::kAtom, 1024);
+      uint32_t p[kC];
 #pragma unroll
-      for (int k = 0; k < kC; ++k) b[k] = sdesc_add(d0, k * 2048);
-#pragma unroll
-      for (int g = 0; g < C::kBlocks; ++g) {
-        if (g >= prev_blocks) break;
-        const int jj = it[g] - 1, bb = jj & 1;
-        if (!mbar_wait(bar_pfull(g, bb), (jj >> 1) & 1, ab)) return false;
-        tc_fence_after();
-        uint32_t p[kC];
-#pragma unroll
-        for (int k = 0; k < kC; ++k) p[k] = tmem + 128u * g + (bb ? 64u : 0u) + 8u * k;
-        mma_ts_k(tmem + C::kColO + HD * g, p, b, idO, prev_first ? 0u : 1u);
-        mma_commit(bar_odone(g));
+      for (int k = 0; k < kC; ++k) {
+        b[k] = sdesc_add(v0, vs * C::kTileBytes + k * 2048);
+        p[k] = ts + (bb ? 64u : 0u) + 8u * k;
       }
+      mma_ts_k(to, p, b, idO, prev_first ? 0u : 1u);
+      mma_commit(bar_odone(g));
       mma_commit(bar_vempty + 8u * vs);
       return true;
     };
+    bool pending = false;         // is P V of the tile before still to be issued?
     do {
       // The rows put an item's Q in place once they have read the O before, for
       // which the last product has to be issued first.
-      if (tile > 0 && !issue_pv()) break;
-      const int blocks = w.w.blk.rows > kRows ? C::kBlocks : 1;
-#pragma unroll
-      for (int g = 0; g < C::kBlocks; ++g) {
-        if (g >= blocks) break;
-        ok = ok && mbar_wait(bar_q(g), item[g] & 1, ab);
-        ++item[g];
-      }
-      if (!ok) break;
-      for (; w.t < w.last; ++w.t) {
-        const int ks = tile % C::kKSt;
-        if (!mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab)) { ok = false; break; }
-        uint64_t b[kD];
-        const uint64_t d0 = sdesc_sw128(sb + C::kOffK + ks * C::kTileBytes, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < kD; ++k) b[k] = sdesc_add(d0, (k >> 2) * C::kAtom + (k & 3) * 32);
-        const uint64_t x0 = sdesc_plain(sb + C::kOffKEx + ks * C::kKEx, 128, C::kExRow8);
-#pragma unroll
-        for (int g = 0; g < C::kBlocks; ++g) {
-          if (g >= blocks) break;
-          const int bb = it[g] & 1;
-          // S over P of two tiles before: its product has to be complete.  (At
-          // an item's first tile the wait for Q has shown more than that, and
-          // the phase waited for here may be over already.)
-          if (it[g] >= 2 && w.t > w.first && !mbar_wait(bar_odone(g), (it[g] - 2) & 1, ab)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          uint64_t q[kD];
-          const uint64_t q0 = sdesc_sw128(sb + C::kOffQ + g * C::kQTile, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < kD; ++k) q[k] = sdesc_add(q0, (k >> 2) * C::kQAtom + (k & 3) * 32);
-          const uint32_t dst = tmem + 128u * g + (bb ? 64u : 0u);
-          mma_ss_k(dst, q, b, idS, 0u);
-          const uint64_t qx = sdesc_plain(sb + C::kOffQEx + g * C::kQEx, 128, C::kExRow8);
-#pragma unroll
-          for (int k = 0; k < C::kExSteps; ++k)
-            mma_ss(dst, sdesc_add(qx, k * 256), sdesc_add(x0, k * 256), idS, 1u);
-          mma_commit(bar_sfull(g, bb));
+      if (pending && !issue_pv()) break;
+      pending = false;
+      if (w.w.blk.rows <= kRows * g) {  // nothing for these rows: the tiles are let go
+        for (; ok && w.t < w.last; ++w.t, ++tile) {
+          const int ks = tile % C::kKSt, vs = tile % C::kVSt;
+          ok = mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab);
+          if (ok) mbar_arrive(bar_kempty + 8u * ks);
+          ok = ok && mbar_wait(bar_vfull + 8u * vs, (tile / C::kVSt) & 1, ab);
+          if (ok) mbar_arrive(bar_vempty + 8u * vs);
         }
-        if (!ok) break;
-        mma_commit(bar_kempty + 8u * ks);
-        if (w.t > w.first && !issue_pv()) { ok = false; break; }
+        continue;
+      }
+      if (!mbar_wait(bar_q(g), item & 1, ab)) break;
+      ++item;
+      for (; w.t < w.last; ++w.t) {
+        const int ks = tile % C::kKSt, bb = it & 1;
+        // S over P of two tiles before: its product has to be complete.  (At an
+        // item's first tile the wait for Q has shown more than that, and the
+        // phase waited for here may be over already.)
+        if (it >= 2 && pending && !mbar_wait(bar_odone(g), (it - 2) & 1, ab)) { ok = false; break; }
+        if (!mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t dst = ts + (bb ? 64u : 0u);
+        {
+          uint64_t q[kD], b[kD];
 #pragma unroll
-        for (int g = 0; g < C::kBlocks; ++g)
-          if (g < blocks) ++it[g];
+          for (int k = 0; k < kD; ++k) {
+            q[k] = sdesc_add(q0, (k >> 2) * C::kQAtom + (k & 3) * 32);
+            b[k] = sdesc_add(k0, ks * C::kTileBytes + (k >> 2) * C::kAtom + (k & 3) * 32);
+          }
+          mma_ss_k(dst, q, b, idS, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < C::kExSteps; ++k)
+          mma_ss(dst, sdesc_add(qx, k * 256), sdesc_add(kx, ks * C::kKEx + k * 256), idS, 1u);
+        mma_commit(bar_sfull(g, bb));
+        mma_commit(bar_kempty + 8u * ks);
+        if (pending && !issue_pv()) { ok = false; break; }
+        ++it;
         ++tile;
         prev_first = w.t == w.first;
-        prev_blocks = blocks;
+        pending = true;
       }
     } while (ok && w.next_item(a));
-    if (ok && tile > 0 && *abort_flag == 0) issue_pv();
-    mma_commit(bar_drain);
-    mbar_wait_drain(bar_drain, 0);
+    if (ok && pending && *abort_flag == 0) issue_pv();
+    mma_commit(bar_drain(g));
+    mbar_wait_drain(bar_drain(g), 0);
   }
 
   tc_fence_before();
