@@ -1,18 +1,23 @@
 // kv4_store.cu -- rows of keys and values into the paged 4-bit cache and back.
 //
 // Append, per (token, head, group of channels): m = min x, s = bf16((max x -
-// m) / 15), code = round((x - m) / s).  x and m are bf16, so m is exact and
-// the code's decision can be exact too: with D = x - m in fp32 the quotient D *
-// (1 / s) gives a candidate, and comparing D with the midpoint (f + 1/2) s,
-// which is exact in fp32 (13 significant bits), decides between f and f + 1.
-// Only where D equals the midpoint can D's own rounding error matter, and then
-// its sign is the sign of that error (two-sum), or a tie.
+// m) / 15), code = round((x - m) / s).  x and m are bf16, so m is exact and the
+// codes can be too: where all of a group's values lie within 2^13 of each other
+// in size (nearly always), D = x - m is exact in fp32 with at most 22
+// significant bits, so that D / s is a midpoint between two codes or at least
+// 2^-22 away from one, relative.  A quotient that is exact where the true one
+// is representable, and off by 2^-24 else, then rounds to the right code; it
+// comes from an approximate one by one correction with its exact remainder
+// (Markstein's method).  The other groups, and those whose range leaves fp32's,
+// take code_of, which compares D with the midpoint.
 //
-// Both kernels move each byte once; a thread holds eight channels (16 bytes of
-// bf16, one 32-bit word of codes) and a group's 4 or 8 threads reduce by shuffles.
+// Minimum and maximum of a group are taken on bf16 pairs in an integer order
+// (two values an instruction), and cross the group's threads in one word.
+//
+// A thread holds eight channels (16 bytes of bf16, one word of codes) of K and
+// of V of two tokens, so that four loads are in flight.  Bound: issue slots
+// (append, about 120 instructions for eight values), HBM (gather).
 #include <cuda_bf16.h>
-
-#include <cfloat>
 
 #include "fa.h"
 #include "kv4.h"
@@ -22,6 +27,7 @@ namespace fa {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kTokens = 2;  // tokens a thread
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -29,11 +35,12 @@ __device__ __forceinline__ float round_bf16(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// The code of x given its group's minimum and scale > 0, inv ~ 1 / scale.
+// The code of x given its group's minimum and scale > 0, inv ~ 1 / scale, for
+// any finite values.
 __device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv) {
   const float D = x - m;
   const float f = fminf(floorf(D * inv), 14.f);
-  const float r = D - (f + 0.5f) * s;
+  const float r = D - (f + 0.5f) * s;  // the midpoint has 13 bits; exact near 0
   bool up = r > 0.f;
   if (r == 0.f) {  // at the midpoint as far as fp32 sees
     const float bb = D - x;
@@ -43,41 +50,79 @@ __device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv
   return static_cast<uint32_t>(static_cast<int>(f)) + (up ? 1u : 0u);
 }
 
-// Quantises this thread's eight channels; `lanes` threads share a group.
+// Two bf16 values as 16-bit integers of the same order, and back (its inverse).
+__device__ __forceinline__ uint32_t ordered(uint32_t w) {
+  return w ^ (((w >> 15) & 0x00010001u) * 0x7fffu);
+}
+
+// Quantises this thread's eight channels; kLanes threads share a group.
 // Returns the word of codes, and the group's param in *param.
 template <int kLanes>
 __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t* param) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  float x[8];
-  float lo = FLT_MAX, hi = -FLT_MAX;
-  bool odd = false;  // NaN or infinity
+  // Largest value, largest of the negated order (the smallest value), and the
+  // smallest size above zero (sizes moved by 0x7fff: zero is then the top of
+  // the signed range, and no half carries into the other).
+  uint32_t top = ordered(w[0]), bot = ~top, least = 0x7fff7fffu;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-    odd = odd || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-    lo = fminf(lo, fminf(x[2 * i], x[2 * i + 1]));
-    hi = fmaxf(hi, fmaxf(x[2 * i], x[2 * i + 1]));
+  for (int i = 1; i < 4; ++i) {
+    const uint32_t o = ordered(w[i]);
+    top = __vmaxs2(top, o);
+    bot = __vmaxs2(bot, ~o);
   }
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-    odd = __shfl_xor_sync(0xffffffffu, odd ? 1 : 0, d) || odd;
-  }
-  if (odd) {
+  for (int i = 0; i < 4; ++i) least = __vmins2(least, (w[i] & 0x7fff7fffu) + 0x7fff7fffu);
+  // (largest, largest negated) of the halves, then of the group's threads
+  uint32_t both = __vmaxs2(__byte_perm(top, bot, 0x5410), __byte_perm(top, bot, 0x7632));
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) both = __vmaxs2(both, __shfl_xor_sync(0xffffffffu, both, d));
+  const uint32_t range = ordered(both ^ 0xffff0000u);  // low: largest, high: smallest, bf16
+  const float hi = bf16_lo(range), lo = bf16_hi(range);
+  const float big = fmaxf(fabsf(lo), fabsf(hi));
+  // An infinity, or a NaN: one of either sign is the largest or the smallest.
+  if (!(big < INFINITY)) {
     *param = 0x7fc07fc0u;
     return 0;
+  }
+  const float span = hi - lo;
+  // One below the smallest size, NaN if there is none.
+  float small = __uint_as_float(min((least & 0xffffu) - 0x8000u, (least >> 16) - 0x8000u) << 16);
+  if (lo != 0.f) small = fminf(small, fabsf(lo));
+  const bool near = big < 0x1p125f && span > 0x1p-60f && !(small < 0x1p-13f * big);
+  if (near) {
+    const float s = round_bf16(__fdiv_rn(span, 15.f));
+    *param = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint64_t m2 = f2_pack(lo, lo), s2 = f2_pack(-s, -s), i2 = f2_pack(inv, inv);
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a sum's low bits are the integer
+    const uint64_t magic = f2_pack(kMagic, kMagic);
+    uint32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t D = f2_sub(f2_pack(bf16_lo(w[i]), bf16_hi(w[i])), m2);
+      const uint64_t q = f2_mul(D, i2);
+      const uint64_t r = f2_fma(q, s2, D);
+      float a, b;
+      f2_unpack(f2_add(f2_fma(r, i2, q), magic), a, b);
+      t[2 * i] = __float_as_uint(a);
+      t[2 * i + 1] = __float_as_uint(b);
+    }
+    // Nibble p holds channel 2 p, nibble 4 + p channel 2 p + 1.  The integers
+    // still carry the bits of kMagic: their sum is taken off at the end.
+    uint32_t codes = 0;
+#pragma unroll
+    for (int p = 7; p >= 0; --p) codes = codes * 16u + t[p < 4 ? 2 * p : 2 * (p - 4) + 1];
+    return codes - 0x4b400000u * 0x11111111u;
   }
   // The difference of finite values can pass fp32's range, and a subnormal
   // scale has no reciprocal: such groups are scaled by a power of two first
   // (exact).
-  const float big = fmaxf(fabsf(lo), fabsf(hi));
   float up = 1.f, down = 1.f;
-  if (big > 0x1p125f) {
+  if (big >= 0x1p125f) {
     up = 0x1p-4f;
     down = 0x1p4f;
-  } else if (hi - lo < 0x1p-60f) {
+  } else if (span <= 0x1p-60f) {
     up = 0x1p64f;
     down = 0x1p-64f;
   }
@@ -88,44 +133,57 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t* param) {
   const float s = s_true * up;
   const float inv = __frcp_rn(s);
   uint32_t codes = 0;
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    codes |= code_of(x[c] * up, m, s, inv) << (4 * ((c & 1) * 4 + c / 2));
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+    codes |= code_of(bf16_lo(x) * up, m, s, inv) << (4 * i);
+    codes |= code_of(bf16_hi(x) * up, m, s, inv) << (4 * i + 16);
+  }
   return codes;
 }
 
-// grid (token blocks, heads); a block holds kRowThreads / (d / 8) tokens.
+// grid (token blocks, heads); a block holds kTokens * kRowThreads / (d / 8) tokens.
 template <int kGroup>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
   const int tpr = a.d / 8;  // threads a row: 8, 16 or 32, so a warp holds whole rows
-  const int t = blockIdx.x * (kRowThreads / tpr) + threadIdx.x / tpr;
+  const int pass = kRowThreads / tpr;
+  const int t0 = blockIdx.x * (kTokens * pass) + threadIdx.x / tpr;
   const int part = threadIdx.x % tpr;
   const int h = blockIdx.y;
-  int slot = -1;
-  if (t < a.T) slot = a.slots[t];
-  if (slot < -1 || slot >= a.num_slots) {
-    atomicCAS(a.input_err, 0, FA_ERR_INVALID_ARG);
-    slot = -1;
+  int slot[kTokens];
+  uint4 k[kTokens], v[kTokens];
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = t0 + i * pass;
+    slot[i] = t < a.T ? a.slots[t] : -1;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    if (t < a.T) {
+      k[i] = __ldg(reinterpret_cast<const uint4*>(a.k_in + static_cast<long long>(t) * a.k_ts +
+                                                  static_cast<long long>(h) * a.k_hs) + part);
+      v[i] = __ldg(reinterpret_cast<const uint4*>(a.v_in + static_cast<long long>(t) * a.v_ts +
+                                                  static_cast<long long>(h) * a.v_hs) + part);
+    }
   }
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (slot >= 0) {
-    k = __ldg(reinterpret_cast<const uint4*>(a.k_in + static_cast<long long>(t) * a.k_ts +
-                                             static_cast<long long>(h) * a.k_hs) + part);
-    v = __ldg(reinterpret_cast<const uint4*>(a.v_in + static_cast<long long>(t) * a.v_ts +
-                                             static_cast<long long>(h) * a.v_hs) + part);
-  }
-  uint32_t kp, vp;
-  const uint32_t kc = quantise8<kGroup / 8>(k, &kp);
-  const uint32_t vc = quantise8<kGroup / 8>(v, &vp);
-  if (slot < 0) return;
-  const int off = slot & ((1 << a.lay.page_shift) - 1);
-  uint8_t* rec = a.cache + (static_cast<long long>(slot >> a.lay.page_shift) * a.Hkv + h) * a.lay.record;
-  *reinterpret_cast<uint32_t*>(rec + off * a.lay.code_row + part * 4) = kc;
-  *reinterpret_cast<uint32_t*>(rec + a.lay.v_codes + off * a.lay.code_row + part * 4) = vc;
-  if (part % (kGroup / 8) == 0) {
-    const int g = part / (kGroup / 8);
-    *reinterpret_cast<uint32_t*>(rec + a.lay.k_params + off * a.lay.param_row + g * 4) = kp;
-    *reinterpret_cast<uint32_t*>(rec + a.lay.v_params + off * a.lay.param_row + g * 4) = vp;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    if (slot[i] < -1 || slot[i] >= a.num_slots) {
+      atomicCAS(a.input_err, 0, FA_ERR_INVALID_ARG);
+      slot[i] = -1;
+    }
+    uint32_t kp, vp;
+    const uint32_t kc = quantise8<kGroup / 8>(k[i], &kp);
+    const uint32_t vc = quantise8<kGroup / 8>(v[i], &vp);
+    if (slot[i] < 0) continue;
+    const int off = slot[i] & ((1 << a.lay.page_shift) - 1);
+    uint8_t* rec =
+        a.cache + (static_cast<long long>(slot[i] >> a.lay.page_shift) * a.Hkv + h) * a.lay.record;
+    *reinterpret_cast<uint32_t*>(rec + off * a.lay.code_row + part * 4) = kc;
+    *reinterpret_cast<uint32_t*>(rec + a.lay.v_codes + off * a.lay.code_row + part * 4) = vc;
+    if (part % (kGroup / 8) == 0) {
+      const int g = part / (kGroup / 8);
+      *reinterpret_cast<uint32_t*>(rec + a.lay.k_params + off * a.lay.param_row + g * 4) = kp;
+      *reinterpret_cast<uint32_t*>(rec + a.lay.v_params + off * a.lay.param_row + g * 4) = vp;
+    }
   }
 }
 
@@ -142,33 +200,43 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t param) {
 template <int kGroup>
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4RowsArgs a) {
   const int tpr = a.d / 8;
-  const int t = blockIdx.x * (kRowThreads / tpr) + threadIdx.x / tpr;
+  const int pass = kRowThreads / tpr;
+  const int t0 = blockIdx.x * (kTokens * pass) + threadIdx.x / tpr;
   const int part = threadIdx.x % tpr;
   const int h = blockIdx.y;
-  if (t >= a.T) return;
-  const int slot = a.slots[t];
-  if (slot < 0 || slot >= a.num_slots) {
-    if (slot != -1) atomicCAS(a.input_err, 0, FA_ERR_INVALID_ARG);
-    return;
-  }
-  const int off = slot & ((1 << a.lay.page_shift) - 1);
   const int g = part / (kGroup / 8);
-  const uint8_t* rec =
-      a.cache + (static_cast<long long>(slot >> a.lay.page_shift) * a.Hkv + h) * a.lay.record;
-  const uint32_t kc = *reinterpret_cast<const uint32_t*>(rec + off * a.lay.code_row + part * 4);
-  const uint32_t vc =
-      *reinterpret_cast<const uint32_t*>(rec + a.lay.v_codes + off * a.lay.code_row + part * 4);
-  const uint32_t kp =
-      *reinterpret_cast<const uint32_t*>(rec + a.lay.k_params + off * a.lay.param_row + g * 4);
-  const uint32_t vp =
-      *reinterpret_cast<const uint32_t*>(rec + a.lay.v_params + off * a.lay.param_row + g * 4);
-  const long long out = (static_cast<long long>(t) * a.Hkv + h) * tpr + part;
-  reinterpret_cast<uint4*>(a.k_out)[out] = values8(kc, kp);
-  reinterpret_cast<uint4*>(a.v_out)[out] = values8(vc, vp);
+  int slot[kTokens];
+  uint32_t kc[kTokens], vc[kTokens], kp[kTokens], vp[kTokens];
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) slot[i] = t0 + i * pass < a.T ? a.slots[t0 + i * pass] : -1;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    if (slot[i] < -1 || slot[i] >= a.num_slots) {
+      atomicCAS(a.input_err, 0, FA_ERR_INVALID_ARG);
+      slot[i] = -1;
+    }
+    if (slot[i] < 0) continue;
+    const int off = slot[i] & ((1 << a.lay.page_shift) - 1);
+    const uint8_t* rec =
+        a.cache + (static_cast<long long>(slot[i] >> a.lay.page_shift) * a.Hkv + h) * a.lay.record;
+    const uint8_t* c = rec + off * a.lay.code_row + part * 4;
+    const uint8_t* p = rec + off * a.lay.param_row + g * 4;
+    kc[i] = *reinterpret_cast<const uint32_t*>(c);
+    vc[i] = *reinterpret_cast<const uint32_t*>(c + a.lay.v_codes);
+    kp[i] = *reinterpret_cast<const uint32_t*>(p + a.lay.k_params);
+    vp[i] = *reinterpret_cast<const uint32_t*>(p + a.lay.v_params);
+  }
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    if (slot[i] < 0) continue;
+    const long long out = (static_cast<long long>(t0 + i * pass) * a.Hkv + h) * tpr + part;
+    reinterpret_cast<uint4*>(a.k_out)[out] = values8(kc[i], kp[i]);
+    reinterpret_cast<uint4*>(a.v_out)[out] = values8(vc[i], vp[i]);
+  }
 }
 
 dim3 rows_grid(const Kv4RowsArgs& a) {
-  const int per = kRowThreads / (a.d / 8);
+  const int per = kTokens * (kRowThreads / (a.d / 8));
   return dim3(static_cast<unsigned>((a.T + per - 1) / per), static_cast<unsigned>(a.Hkv));
 }
 

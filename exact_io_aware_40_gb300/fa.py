@@ -371,48 +371,46 @@ def _need(t, name, dtype, shape, dev):
     """Checks a contiguous tensor on CUDA device number `dev`."""
     if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _expect(t, name, dtype, tuple(shape))
-        raise ValueError("all tensors must be on one CUDA device, got %s on cuda:%d and %s on cuda:%d"
-                         % (name, t.get_device(), "others", dev))
+        raise ValueError("all tensors must be on one CUDA device, %s is on cuda:%d and not cuda:%d"
+                         % (name, t.get_device(), dev))
 
 
-def _need_rows(t, name, shape, dev):
-    """Checks a bf16 [tokens, heads, d] tensor of any strides the kernels take; returns its
-    token and head strides."""
-    import torch
+def _need_rows(t, name, dtype, shape, dev):
+    """Checks a [tokens, heads, d] tensor of any strides the kernels take; returns its token
+    and head strides."""
     ts, hs, cs = t.stride()
-    if t.dtype != torch.bfloat16 or t.shape != shape or cs != 1 or t.get_device() != dev:
-        raise ValueError("%s must be a torch.bfloat16 tensor of shape %s with contiguous channels "
-                         "on the CUDA device of the others" % (name, tuple(shape)))
-    ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
-    if ts % 8 or hs % 8 or max(ts, hs) > 0x7fffffff or t.data_ptr() % 16:
-        raise ValueError("%s: strides must be multiples of 8 elements (below 2^31) and the data "
-                         "16-byte aligned" % name)
+    if t.dtype != dtype or t.shape != shape or cs != 1 or t.get_device() != dev:
+        raise ValueError("%s must be a %s tensor of shape %s with contiguous channels on the CUDA "
+                         "device of the others" % (name, dtype, tuple(shape)))
+    if (ts | hs) & 7 or ts > 0x7fffffff or hs > 0x7fffffff or t.data_ptr() & 15:
+        ts, hs = ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0  # unused strides are free
+        if (ts | hs) & 7 or ts > 0x7fffffff or hs > 0x7fffffff or t.data_ptr() & 15:
+            raise ValueError("%s: strides must be multiples of 8 elements (below 2^31) and the "
+                             "data 16-byte aligned" % name)
     return ts, hs
 
 
-def _need_cache(cache, page_size, d, group):
+def _need_cache(cache, dtype, page_size, d, group):
     """Checks a cache tensor against its geometry; returns (num_pages, kv_heads, device)."""
-    import torch
     if cache.dim() != 3:
         raise ValueError("expected a [num_pages, kv_heads, page bytes] cache")
     pages, heads, record = cache.shape
-    if (record != kv4_page_bytes(d, page_size, group) or cache.dtype != torch.uint8
-            or not cache.is_cuda or not cache.is_contiguous()):
-        _expect(cache, "cache", torch.uint8, (pages, heads, kv4_page_bytes(d, page_size, group)))
-    return pages, heads, cache.get_device()
+    dev = cache.get_device()
+    want = _KV4_RECORD.get((d, page_size, group)) or kv4_page_bytes(d, page_size, group)
+    if record != want or cache.dtype != dtype or dev < 0 or not cache.is_contiguous():
+        _expect(cache, "cache", dtype, (pages, heads, want))
+    return pages, heads, dev
 
 
-def _enqueue(dev, stream, call):
-    """call(raw stream) with device `dev` current, and `stream` (a raw stream) if one is given:
-    what the call allocates then belongs to the stream that uses it."""
+def _elsewhere(dev, stream, call, *args, **kwargs):
+    """call(*args) with device number `dev` current, and `stream` (a raw stream) if one is
+    given: what the call allocates then belongs to the stream that uses it."""
     import torch
-    if stream is not None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
-            return call(int(stream))
-    if torch.cuda.current_device() == dev:
-        return call(torch._C._cuda_getCurrentRawStream(dev))
-    with torch.cuda.device(dev):
-        return call(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is None:
+        with torch.cuda.device(dev):
+            return call(*args, **kwargs)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
+        return call(*args, **kwargs)
 
 
 def kv4_plan(past_len, new_len, block_table, free_list, free_state, page_size, max_tokens,
@@ -422,37 +420,38 @@ def kv4_plan(past_len, new_len, block_table, free_list, free_state, page_size, m
     past_len, new_len: CUDA int32 [B] (new_len -1: the request is finished); block_table int32
     [B, max_pages] and free_list int32 [num_pages] are updated in place; free_state int32 [>= 2]
     (first free entry, number): the state an earlier call returned.  Returns (kv_len [B],
-    cu_q [B + 1], slots [max_tokens], state [4]), views of one buffer."""
+    cu_q [B + 1], slots [max_tokens], state [4])."""
     import torch
     if block_table.dim() != 2:
         raise ValueError("expected a [B, max_pages] block_table")
     B, max_pages = block_table.shape
-    n = free_list.numel()
-    if num_pages is not None and num_pages != n:
-        raise ValueError("free_list must hold num_pages entries")
+    n, state_n = free_list.numel(), free_state.numel()
     dev, i32 = past_len.get_device(), torch.int32
+    if dev < 0:
+        raise ValueError("past_len must be a CUDA tensor")
     _need(past_len, "past_len", i32, (B,), dev)
     _need(new_len, "new_len", i32, (B,), dev)
     _need(block_table, "block_table", i32, (B, max_pages), dev)
     _need(free_list, "free_list", i32, (n,), dev)
-    state_n = free_state.numel()
     _need(free_state, "free_state", i32, (state_n,), dev)
-    if dev < 0:
-        raise ValueError("past_len must be a CUDA tensor")
-    if state_n < 2 or max_tokens < 1:
-        raise ValueError("free_state must hold the first free entry and their number, and "
-                         "max_tokens be positive")
-
-    def call(raw):
-        out = torch.empty(2 * B + 5 + max_tokens, dtype=i32, device=past_len.device)
-        at = out.data_ptr()
-        _check(load_library().fa_kv4_plan(
-            past_len.data_ptr(), new_len.data_ptr(), B, page_size, n, block_table.data_ptr(),
-            max_pages, free_list.data_ptr(), free_state.data_ptr(), max_tokens, at, at + 4 * B,
-            at + 4 * (2 * B + 1), at + 4 * (2 * B + 1 + max_tokens), raw), "fa_kv4_plan")
-        return out
-
-    return _enqueue(dev, stream, call).split_with_sizes((B, B + 1, max_tokens, 4))
+    if state_n < 2 or not 1 <= max_tokens <= 0x7fffffff or (num_pages is not None and num_pages != n):
+        raise ValueError("free_state must hold the first free entry and their number, free_list "
+                         "num_pages entries, and max_tokens be positive")
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, kv4_plan, past_len, new_len, block_table, free_list,
+                          free_state, page_size, max_tokens)
+    at = past_len.device
+    kv_len = torch.empty(B, dtype=i32, device=at)
+    cu_q = torch.empty(B + 1, dtype=i32, device=at)
+    slots = torch.empty(max_tokens, dtype=i32, device=at)
+    state = torch.empty(4, dtype=i32, device=at)
+    status = load_library().fa_kv4_plan(
+        past_len.data_ptr(), new_len.data_ptr(), B, page_size, n, block_table.data_ptr(), max_pages,
+        free_list.data_ptr(), free_state.data_ptr(), max_tokens, kv_len.data_ptr(), cu_q.data_ptr(),
+        slots.data_ptr(), state.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise FAError(status, "fa_kv4_plan")
+    return kv_len, cu_q, slots, state
 
 
 def kv4_append(k, v, slots, cache, page_size, group=32, stream=None):
@@ -461,26 +460,30 @@ def kv4_append(k, v, slots, cache, page_size, group=32, stream=None):
     import torch
     if k.dim() != 3 or v.dim() != 3:
         raise ValueError("expected [T, kv_heads, d] keys and values")
-    shape = k.shape
+    shape, bf16 = k.shape, torch.bfloat16
     T, heads, d = shape
-    pages, cache_heads, dev = _need_cache(cache, page_size, d, group)
+    pages, cache_heads, dev = _need_cache(cache, torch.uint8, page_size, d, group)
     if heads != cache_heads:
         raise ValueError("k has %d heads, the cache %d" % (heads, cache_heads))
-    k_ts, k_hs = _need_rows(k, "k", shape, dev)
-    v_ts, v_hs = _need_rows(v, "v", shape, dev)
+    k_ts, k_hs = _need_rows(k, "k", bf16, shape, dev)
+    v_ts, v_hs = _need_rows(v, "v", bf16, shape, dev)
     _need(slots, "slots", torch.int32, (T,), dev)
     if T == 0:
         return
-    _enqueue(dev, stream, lambda raw: _check(load_library().fa_kv4_append(
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, kv4_append, k, v, slots, cache, page_size, group)
+    status = load_library().fa_kv4_append(
         k.data_ptr(), v.data_ptr(), T, heads, d, k_ts, k_hs, v_ts, v_hs, slots.data_ptr(),
-        cache.data_ptr(), pages, page_size, group, raw), "fa_kv4_append"))
+        cache.data_ptr(), pages, page_size, group, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise FAError(status, "fa_kv4_append")
 
 
 def kv4_gather(slots, cache, page_size, d, group=32, out_k=None, out_v=None, stream=None):
     """The values the cache holds at `slots` (CUDA int32 [T]): bf16 (K, V), each
     [T, kv_heads, d].  Rows whose slot is -1 are not written (fa_kv4_gather)."""
     import torch
-    pages, heads, dev = _need_cache(cache, page_size, d, group)
+    pages, heads, dev = _need_cache(cache, torch.uint8, page_size, d, group)
     T = slots.numel()
     bf16, shape = torch.bfloat16, (T, heads, d)
     _need(slots, "slots", torch.int32, (T,), dev)
@@ -488,17 +491,19 @@ def kv4_gather(slots, cache, page_size, d, group=32, out_k=None, out_v=None, str
         _need(out_k, "out_k", bf16, shape, dev)
     if out_v is not None:
         _need(out_v, "out_v", bf16, shape, dev)
-
-    def call(raw):
-        K = torch.empty(shape, dtype=bf16, device=cache.device) if out_k is None else out_k
-        V = torch.empty(shape, dtype=bf16, device=cache.device) if out_v is None else out_v
-        if T:
-            _check(load_library().fa_kv4_gather(
-                slots.data_ptr(), cache.data_ptr(), pages, page_size, group, T, heads, d,
-                K.data_ptr(), V.data_ptr(), raw), "fa_kv4_gather")
-        return K, V
-
-    return _enqueue(dev, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, kv4_gather, slots, cache, page_size, d, group, out_k, out_v)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=bf16, device=cache.device)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=bf16, device=cache.device)
+    if T:
+        status = load_library().fa_kv4_gather(
+            slots.data_ptr(), cache.data_ptr(), pages, page_size, group, T, heads, d,
+            out_k.data_ptr(), out_v.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+        if status:
+            raise FAError(status, "fa_kv4_gather")
+    return out_k, out_v
 
 
 def kv4_attention_workspace_bytes(q_heads, kv_heads, d, max_q):
@@ -519,45 +524,47 @@ def kv4_attention(q, cache, block_table, cu_q, kv_len, max_q, page_size, group=3
     import torch
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("expected [total_q, q_heads, d] queries and a [B, max_pages] block_table")
-    shape = q.shape
+    shape, bf16, i32 = q.shape, torch.bfloat16, torch.int32
     total, q_heads, d = shape
-    pages, kv_heads, dev = _need_cache(cache, page_size, d, group)
+    pages, kv_heads, dev = _need_cache(cache, torch.uint8, page_size, d, group)
     B, max_pages = block_table.shape
-    i32 = torch.int32
-    q_ts, q_hs = _need_rows(q, "q", shape, dev)
+    q_ts, q_hs = _need_rows(q, "q", bf16, shape, dev)
     if q_heads % kv_heads:
         raise ValueError("%d query heads do not divide into %d K/V heads" % (q_heads, kv_heads))
-    if max_q < 1:
-        raise ValueError("max_q must be positive")
+    if not 1 <= max_q <= 0x7fffffff or not -1 <= window <= 0x7fffffff or total > 0x7fffffff:
+        raise ValueError("max_q must be positive, window at least -1, and sizes below 2^31")
     _need(block_table, "block_table", i32, (B, max_pages), dev)
     _need(cu_q, "cu_q", i32, (B + 1,), dev)
     _need(kv_len, "kv_len", i32, (B,), dev)
     if out is not None:
-        _need(out, "out", torch.bfloat16, shape, dev)
+        _need(out, "out", bf16, shape, dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, q_heads), dev)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-
-    def call(raw):
-        at = q.device
-        O = torch.empty(shape, dtype=torch.bfloat16, device=at) if out is None else out
-        L = torch.empty((total, q_heads), dtype=torch.float32, device=at) if lse is None else lse
-        if total and B:
-            lib = load_library()
-            ws = workspace
-            if ws is None:
-                ws = torch.empty(lib.fa_kv4_attn_workspace_bytes(q_heads, kv_heads, d, max_q),
-                                 dtype=torch.uint8, device=at)
-            _check(lib.fa_kv4_attn(
-                q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                kv_len.data_ptr(), O.data_ptr(), L.data_ptr(), B, total, max_q, q_heads, kv_heads, d,
-                q_ts, q_hs, pages, max_pages, page_size, group,
-                1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, window,
-                ws.data_ptr(), ws.numel(), raw), "fa_kv4_attn")
-        return O, L
-
-    return _enqueue(dev, stream, call)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, kv4_attention, q, cache, block_table, cu_q, kv_len, max_q,
+                          page_size, group, causal, scale, window, out, lse, workspace)
+    at = q.device
+    if out is None:
+        out = torch.empty(shape, dtype=bf16, device=at)
+    if lse is None:
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=at)
+    if total == 0 or B == 0:
+        return out, lse
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(lib.fa_kv4_attn_workspace_bytes(q_heads, kv_heads, d, max_q),
+                                dtype=torch.uint8, device=at)
+    status = lib.fa_kv4_attn(
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), B, total, max_q, q_heads, kv_heads, d, q_ts, q_hs, pages,
+        max_pages, page_size, group, 1.0 / math.sqrt(d) if scale is None else float(scale),
+        1 if causal else 0, window, workspace.data_ptr(), workspace.numel(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise FAError(status, "fa_kv4_attn")
+    return out, lse
 
 
 # ------------------------------------------------------------------ autograd
