@@ -21,7 +21,8 @@
 // fp16, as Q is (8 bits) after a scaling of each row by a power of two.  The
 // rest of a key, minimum + 8 scale of each group, meets the sum of Q over the
 // group; both are split into two fp16 (22 bits) and their three leading products
-// are slots of one more k-step (two if there are eight groups).  So scores have
+// are slots of one more k-step (two if there are eight groups): minima (h, l) by
+// group, then h again, against sums (h, h), then l.  So scores have
 // the accuracy of fp32 sums without a second pass over K.
 // V.  minimum + scale * code rounded to fp16, P in fp16: see kv4_attn.cu.
 // fp16's range: the K and V of a tile are taken in units of a power of two that
@@ -47,7 +48,7 @@ constexpr int kTile = 64;
 constexpr float kGrow = 4.f;
 constexpr float kShift = 10.f;
 constexpr float kLn2f = 0.693147180559945309f;
-constexpr int kUnits = 4;  // ring of tile units: a tile's is read before tile + 4 is converted
+constexpr int kUnits = 8;  // ring of tile units: K's converter is at most five tiles ahead of the rows
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -85,6 +86,11 @@ __device__ __forceinline__ bool odd_param(uint32_t p) {
 }
 __device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float param_min(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -148,8 +154,8 @@ struct Cfg {
   // Registers a thread of the warpgroups (rows, each converter, products) out
   // of the launch's.
   static constexpr int kLaunchRegs = kBlocks == 2 ? 96 : 128;
-  static constexpr int kRowRegs = kBlocks == 2 ? 144 : 208;
-  static constexpr int kConvRegs = kBlocks == 2 ? 64 : 104;
+  static constexpr int kRowRegs = kBlocks == 2 ? 128 : 208;
+  static constexpr int kConvRegs = kBlocks == 2 ? 80 : 104;
   static constexpr int kMmaRegs = kBlocks == 2 ? 64 : 96;
   static_assert(kBlocks * kRowRegs + 2 * kConvRegs + kMmaRegs <= (kBlocks + 3) * kLaunchRegs, "register split");
 };
@@ -213,9 +219,10 @@ struct Units {
   int meta[2][8];                // of a converter's tiles: bit 0 edge, bit 1 item's first
 };
 
-// The converter of K (kSide 0) or V (1): four warps; `w` is its own walk.
+// The converter of K (kSide 0) or V (1): four warps.  `walk` is the warp's own,
+// in shared memory: it is touched once an item and would only take registers.
 template <int HD, int GROUP, int kSide>
-__device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROUP>::kBlockRows>& w,
+__device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROUP>::kBlockRows>& walk,
                                         uint8_t* smem, uint32_t sb, uint32_t bar_full,
                                         uint32_t bar_empty, Units& un, const Abort& ab) {
   using C = Cfg<HD, GROUP>;
@@ -225,48 +232,69 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   const int part = ct % C::kTpr;   // 32-channel block
   const int ptok = ct / C::kTpr;   // token of a pass
   const int group = part * 32 / GROUP;
-  const int total = static_cast<int>(w.u_end - w.u);
-  const int codes_at = kSide ? a.lay.v_codes : 0, params_at = kSide ? a.lay.v_params : a.lay.k_params;
+  __syncwarp();
+  const int total = static_cast<int>(walk.u_end - walk.u);
+  const long long page_bytes = static_cast<long long>(a.Hkv) * a.lay.record;
+  const int shift = a.lay.page_shift, in_page = (1 << shift) - 1;
   // This thread's place in the ring: codes of pass p of tile n, then params.
   uint8_t* ring = smem + C::kOffRing + kSide * C::kRing * C::kRingTile;
   const uint32_t ring_u32 = sb + C::kOffRing + kSide * C::kRing * C::kRingTile;
   auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + ct * 16; };
   auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + 2048 + ct * 4; };
-  int pages[C::kPasses];  // of the tile w stands at, the next to be copied
+  // Of the item the next tile to be copied belongs to:
+  const int* table;           // its request's row of the block table
+  const uint8_t *codes, *params;  // this thread's, of token 0 of page 0
+  int key, key_end, hi, all_hi, all_lo;
+  bool opening;               // that tile is its item's first
+  auto open = [&]() {
+    __syncwarp();
+    const auto& w = walk;
+    table = a.table + static_cast<long long>(w.w.b) * a.max_pages;
+    const uint8_t* rec = a.cache + static_cast<long long>(w.w.h) * a.lay.record;
+    codes = rec + (kSide ? a.lay.v_codes : 0) + part * 16;
+    params = rec + (kSide ? a.lay.v_params : a.lay.k_params) + group * 4;
+    key = (w.w.blk.tile_lo + w.first) * kTile;
+    key_end = (w.w.blk.tile_lo + w.last) * kTile;
+    hi = w.w.blk.hi;
+    all_hi = w.w.blk.all_hi;
+    all_lo = w.w.blk.all_lo;
+    opening = true;
+    __syncwarp();
+  };
+  int pages[C::kPasses];      // of that tile
   auto locate = [&]() {
-    const int key = (w.w.blk.tile_lo + w.t) * kTile;
 #pragma unroll
     for (int p = 0; p < C::kPasses; ++p) {
       const int tok = key + p * C::kPassTokens + ptok;
-      pages[p] = -1;
-      if (tok < w.w.blk.hi)
-        pages[p] = __ldg(a.table + static_cast<long long>(w.w.b) * a.max_pages +
-                         (tok >> a.lay.page_shift));
+      pages[p] = 0;
+      // volatile: issued here, an iteration before it is used
+      if (tok < hi) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(pages[p]) : "l"(table + (tok >> shift)));
     }
   };
   auto copy = [&](int n) {
     if (n < total) {
-      const int key = (w.w.blk.tile_lo + w.t) * kTile;
       if (ct == 0)
-        un.meta[kSide][n & 7] = (key + kTile > w.w.blk.all_hi || key < w.w.blk.all_lo ? 1 : 0) |
-                                (w.t == w.first ? 2 : 0);
+        un.meta[kSide][n & 7] = (key + kTile > all_hi || key < all_lo ? 1 : 0) | (opening ? 2 : 0);
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
         const int tok = key + p * C::kPassTokens + ptok;
-        const bool have = tok < w.w.blk.hi;
         int pg = pages[p];
-        if (pg < 0 || pg >= a.num_pages) {
-          if (have) atomicCAS(a.input_err, 0, 1);
+        if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages)) {
+          atomicCAS(a.input_err, 0, 1);
           pg = 0;
         }
-        const int off = tok & ((1 << a.lay.page_shift) - 1);
-        const uint8_t* rec = a.cache + (static_cast<long long>(pg) * a.Hkv + w.w.h) * a.lay.record;
-        cp_async16(ring_u32 + ring16(n, p), rec + codes_at + off * C::kCodeRow + part * 16, have);
-        cp_async4(ring_u32 + ring4(n, p), rec + params_at + off * C::kParamRow + group * 4, have);
+        const int off = tok & in_page;
+        const long long at = pg * page_bytes;
+        cp_async16(ring_u32 + ring16(n, p), codes + at + off * C::kCodeRow, tok < hi);
+        cp_async4(ring_u32 + ring4(n, p), params + at + off * C::kParamRow, tok < hi);
       }
-      bool more = true;
-      if (++w.t >= w.last) more = w.next_item(a);
-      if (more) locate();
+      opening = false;
+      key += kTile;
+      if (key >= key_end && n + 1 < total) {
+        if (lane == 0) walk.next_item(a);
+        open();
+      }
+      if (n + 1 < total) locate();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -303,6 +331,7 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
 
   int e_run = 0;  // V's unit so far in the item
   bool ok = true;
+  open();
   locate();
   for (int n = 0; n < C::kRing - 1; ++n) copy(n);
   asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
@@ -371,14 +400,12 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
       }
       if (kSide == 0 && (GROUP == 32 || (part & 1) == 0)) {
         const int tok = p * C::kPassTokens + ptok;
-        const __half h = __float2half_rn(m), l = __float2half_rn(m - __half2float(h));
-        const __half part3[3] = {h, l, h};
+        const __half h = __float2half_rn(m);
         uint8_t* ex = smem + C::kOffKEx + st * C::kKEx + (tok >> 3) * C::kExRow8 + (tok & 7) * 16;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          const int kk = 3 * group + e;
-          *reinterpret_cast<__half*>(ex + (kk >> 3) * 128 + (kk & 7) * 2) = part3[e];
-        }
+        const int k0 = 2 * group, k1 = 2 * C::kGroups + group;
+        *reinterpret_cast<uint32_t*>(ex + (k0 >> 3) * 128 + (k0 & 7) * 2) =
+            pack_f16(m, m - __half2float(h));
+        *reinterpret_cast<__half*>(ex + (k1 >> 3) * 128 + (k1 & 7) * 2) = h;
       }
     }
     fence_proxy_async_smem();
@@ -400,6 +427,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kThreads / 32 + 2];
   __shared__ Units un;
+  __shared__ Tiles<C::kBlockRows> walks[8];  // of the converters' warps
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t pad = ((raw_u32 + 1023u) & ~1023u) - raw_u32;
@@ -528,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
             const __half slot[3] = {h, h, l};
 #pragma unroll
             for (int e = 0; e < 3; ++e) {
-              const int kk = 3 * grp + e;
+              const int kk = e < 2 ? 2 * grp + e : 2 * C::kGroups + grp;
               *reinterpret_cast<__half*>(sqx + (row >> 3) * C::kExRow8 + (kk >> 3) * 128 +
                                          (row & 7) * 16 + (kk & 7) * 2) = slot[e];
             }
@@ -575,7 +603,8 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mxp[e & 3] = fmaxf(mxp[e & 3], __uint_as_float(sr[c][e]));
+          for (int e = 0; e < 32; e += 2)
+            mxp[(e >> 1) & 3] = max3(mxp[(e >> 1) & 3], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
         const float cand = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mult;
         const bool start = w.t == w.first;
         const bool up = cand > m_run + kGrow;
@@ -681,10 +710,12 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
     if (tid == 0) a.split[blockIdx.x] = record;
   } else if (warp < kConvV) {
     regs_dec<C::kConvRegs>();
-    convert<HD, GROUP, 0>(a, w, smem, sb, bar_kfull, bar_kempty, un, ab);
+    if (lane == 0) walks[warp - kConvK] = w;
+    convert<HD, GROUP, 0>(a, walks[warp - kConvK], smem, sb, bar_kfull, bar_kempty, un, ab);
   } else if (warp < kMma) {
     regs_dec<C::kConvRegs>();
-    convert<HD, GROUP, 1>(a, w, smem, sb, bar_vfull, bar_vempty, un, ab);
+    if (lane == 0) walks[warp - kConvK] = w;
+    convert<HD, GROUP, 1>(a, walks[warp - kConvK], smem, sb, bar_vfull, bar_vempty, un, ab);
   } else {
     regs_dec<C::kMmaRegs>();
   }
