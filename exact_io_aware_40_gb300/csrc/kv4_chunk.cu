@@ -34,6 +34,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4.h"
@@ -130,10 +131,11 @@ struct Cfg {
   static constexpr int kExRow8 = kExSteps * 256;  // bytes of eight rows
   static constexpr int kQEx = kRows / 8 * kExRow8, kKEx = kTile / 8 * kExRow8;
   // Converter: threads a token's row of codes, tokens a pass, passes a tile;
-  // tiles of codes in flight or in use, each thread's own 16 + 4 bytes a pass.
+  // tiles of codes in flight or in use, each thread's own 16 + 4 + 4 bytes a
+  // pass (codes, params, K's converter: V's params too).
   static constexpr int kTpr = HD / 32, kPassTokens = 128 / kTpr, kPasses = kTile / kPassTokens;
   static constexpr int kRing = HD == 256 ? 2 : 4;
-  static constexpr int kRingTile = kPasses * 128 * 20;
+  static constexpr int kRingTile = kPasses * 128 * 24;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kBlocks * kQTile;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
@@ -209,13 +211,16 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ha
                : "memory");
 }
 
-// What the converters leave for the rows, by tile (a ring of kUnits).
+// What K's converter leaves for the rows, by tile (a ring of kUnits); it comes
+// to them with the scores.  (V's unit and marks are needed that early, too, so
+// K's converter reads V's params for them; V's converter finds the same unit.)
+// A unit is kept through an item as long as the params fit it.
 struct Units {
   float k_unit[kUnits];          // 2^kexp
   int v_exp[kUnits];
   int any_odd[kUnits];
   uint8_t odd_v[kUnits][kTile];  // groups of a token's V that are not numbers
-  uint32_t top_param[2][2][4];   // [side][tile parity][warp]
+  uint32_t top_param[3][4];      // [K's, V's by K's converter, V's][warp]
   int meta[2][8];                // of a converter's tiles: bit 0 edge, bit 1 item's first
 };
 
@@ -229,8 +234,12 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   constexpr int kSt = kSide ? C::kVSt : C::kKSt;
   constexpr int kBar = C::kBlocks + 1 + kSide;  // named barrier of these four warps
   const int ct = threadIdx.x & 127, cw = ct >> 5, lane = ct & 31;
-  const int part = ct % C::kTpr;   // 32-channel block
-  const int ptok = ct / C::kTpr;   // token of a pass
+  // Token of a pass and 32-channel block: eight lanes side by side write to
+  // different chunks of the swizzled tile (eight tokens, at d = 256 four tokens
+  // of two blocks).
+  constexpr int kTok = HD == 256 ? 4 : 8;  // tokens of those lanes
+  const int part = lane / kTok % C::kTpr;
+  const int ptok = cw * (32 / C::kTpr) + lane / (kTok * C::kTpr) * kTok + lane % kTok;
   const int group = part * 32 / GROUP;
   __syncwarp();
   const int total = static_cast<int>(walk.u_end - walk.u);
@@ -239,8 +248,8 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   // This thread's place in the ring: codes of pass p of tile n, then params.
   uint8_t* ring = smem + C::kOffRing + kSide * C::kRing * C::kRingTile;
   const uint32_t ring_u32 = sb + C::kOffRing + kSide * C::kRing * C::kRingTile;
-  auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + ct * 16; };
-  auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 2560 + 2048 + ct * 4; };
+  auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 3072 + ct * 16; };
+  auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 3072 + 2048 + ct * 4; };
   // Of the item the next tile to be copied belongs to:
   const int* table;           // its request's row of the block table
   const uint8_t *codes, *params;  // this thread's, of token 0 of page 0
@@ -286,7 +295,9 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
         const int off = tok & in_page;
         const long long at = pg * page_bytes;
         cp_async16(ring_u32 + ring16(n, p), codes + at + off * C::kCodeRow, tok < hi);
-        cp_async4(ring_u32 + ring4(n, p), params + at + off * C::kParamRow, tok < hi);
+        const uint8_t* par = params + at + off * C::kParamRow;
+        cp_async4(ring_u32 + ring4(n, p), par, tok < hi);
+        if (kSide == 0) cp_async4(ring_u32 + ring4(n, p) + 512, par + (a.lay.v_params - a.lay.k_params), tok < hi);
       }
       opening = false;
       key += kTile;
@@ -298,82 +309,91 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // Largest params of tile n, numbers only.
-  auto post_top = [&](int n) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int p = 0; p < C::kPasses; ++p) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(ring + ring4(n, p));
-      if (!odd_param(x)) top = __vmaxu2(top, x & 0x7fff7fffu);
-    }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, top >> 16), sc = __reduce_max_sync(0xffffffffu, top & 0xffffu);
-    if (lane == 0) un.top_param[kSide][n & 1][cw] = (m << 16) | sc;
-  };
-  // |minimum| < 2^(e + 14), scale < 2^(e + 10)
-  auto unit_of = [&](int n) -> int {
+  // Byte of the tile where word 0 of pass 0 goes (128-byte swizzle); word i is
+  // chunk i, and a pass later the swizzle is the same.
+  static_assert(C::kPassTokens % 8 == 0, "a pass later the swizzle is the same");
+  const int place = (part >> 1) * C::kAtom + ptok * 128 + ((((part & 1) * 4) ^ (ptok & 7)) << 4);
+
+  // Units: |minimum| < 2^(e + 14), scale < 2^(e + 10).  `limit` holds both bounds
+  // as a param does; params within it need no new unit.
+  auto unit_of = [&](const uint32_t* top) -> int {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, un.top_param[kSide][n & 1][i]);
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, top[i]);
     const int em = static_cast<int>(m >> 23), es = static_cast<int>((m >> 7) & 255);
     return max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
   };
-  // A word of codes is 16 bytes of the tile.  Threads two apart write to the
-  // same banks of neighbouring atoms: every other pair takes its words in
-  // another order.
-  const int flip = (part >> 1) & 1;
-  int place[4];  // byte of the tile where word i of pass 0 goes (128-byte swizzle)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int chunk = part * 4 + (i ^ (flip << 1));
-    place[i] = (chunk >> 3) * C::kAtom + ptok * 128 + (((chunk & 7) ^ (ptok & 7)) << 4);
-  }
-  static_assert(C::kPassTokens % 8 == 0, "a pass later the swizzle is the same");
-
-  int e_run = 0;  // V's unit so far in the item
+  auto limit_of = [&](int e) -> uint32_t {
+    return (static_cast<uint32_t>(min(e + 14 + 127, 255) * 128 - 1) << 16) |
+           (static_cast<uint32_t>(e + 10 + 127) * 128 - 1);
+  };
+  auto post = [&](uint32_t top, int which) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top >> 16), sc = __reduce_max_sync(0xffffffffu, top & 0xffffu);
+    if (lane == 0) un.top_param[which][cw] = (m << 16) | sc;
+  };
+  int e_mine = 0, e_v = 0;                // this side's unit; K's converter: V's
+  uint32_t lim_mine = 0, lim_v = 0;
   bool ok = true;
   open();
   locate();
   for (int n = 0; n < C::kRing - 1; ++n) copy(n);
-  asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
-  post_top(0);
   for (int it = 0; it < total; ++it) {
     const int st = it % kSt, slot = it & (kUnits - 1);
     copy(it + C::kRing - 1);
-    // All four warps posted this tile's largest params (and, on the way, read
-    // the last tile's, so that those may be overwritten).  Every warp passes
-    // here once a tile, so that one that gave up on a wait takes the others
-    // along.
-    ok = bar_and_128(kBar, ok);
-    if (!ok) break;
-    const int flags = un.meta[kSide][it & 7];
-    // K's unit is the tile's own; V's grows only, within an item.
-    e_run = kSide == 0 || (flags & 2) ? unit_of(it) : max(e_run, unit_of(it));
-    const float unit = pow2i(-e_run);
-    if (ct == 0) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 1) : "memory");
+    uint32_t par[C::kPasses], par_v[C::kPasses];
+    uint32_t top = 0, top_v = 0;
+#pragma unroll
+    for (int p = 0; p < C::kPasses; ++p) {
+      par[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p));
+      if (!odd_param(par[p])) top = __vmaxu2(top, par[p] & 0x7fff7fffu);
       if (kSide == 0) {
-        un.k_unit[slot] = pow2i(e_run);
-      } else {
-        un.v_exp[slot] = e_run;
-        un.any_odd[slot] = 0;
+        par_v[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p) + 512);
+        if (!odd_param(par_v[p])) top_v = __vmaxu2(top_v, par_v[p] & 0x7fff7fffu);
       }
     }
-    uint32_t par[C::kPasses];
-#pragma unroll
-    for (int p = 0; p < C::kPasses; ++p) par[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p));
-    if (kSide == 1 && (flags & 1)) {
+    // Do all params fit the units?  Every warp passes here once a tile, so that
+    // one that gave up on a wait takes the others along (a wait is given up
+    // only with the flag set); the flags of the tile are there behind it, too.
+    const bool fits = __vmaxu2(top, lim_mine) == lim_mine && (kSide || __vmaxu2(top_v, lim_v) == lim_v);
+    const bool keep = bar_and_128(kBar, fits && ok);
+    const int flags = un.meta[kSide][it & 7];
+    if (!keep || (flags & 2)) {
+      ok = bar_and_128(kBar, ok && *ab.flag == 0);
+      if (!ok) break;
+      post(top, 2 * kSide);
+      if (kSide == 0) post(top_v, 1);
+      asm volatile("bar.sync %0, 128;" ::"n"(kBar) : "memory");
+      const int e = unit_of(un.top_param[2 * kSide]);
+      e_mine = (flags & 2) ? e : max(e_mine, e);
+      lim_mine = limit_of(e_mine);
+      if (kSide == 0) {
+        const int v = unit_of(un.top_param[1]);
+        e_v = (flags & 2) ? v : max(e_v, v);
+        lim_v = limit_of(e_v);
+      }
+    }
+    const float unit = pow2i(-e_mine);
+    if (kSide == 0 && ct == 0) {
+      un.k_unit[slot] = pow2i(e_mine);
+      un.v_exp[slot] = e_v;
+      un.any_odd[slot] = 0;
+    }
+    if (flags & 1) {
       // Values that are not numbers, where some row does not see them: left out
       // of the product; the rows that see them add them by themselves.
-      asm volatile("bar.sync %0, 128;" ::"n"(kBar) : "memory");  // any_odd is 0
+      if (kSide == 0) asm volatile("bar.sync %0, 128;" ::"n"(kBar) : "memory");  // any_odd is 0
 #pragma unroll
       for (int p = 0; p < C::kPasses; ++p) {
-        const bool odd = odd_param(par[p]);
-        // the token's threads are side by side in the warp
-        uint32_t bits = odd ? 1u << group : 0u;
+        if (kSide == 1) {
+          if (odd_param(par[p])) par[p] = 0;
+        } else {
+          uint32_t bits = odd_param(par_v[p]) ? 1u << group : 0u;
 #pragma unroll
-        for (int d = 1; d < C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
-        if (part == 0) un.odd_v[slot][p * C::kPassTokens + ptok] = static_cast<uint8_t>(bits);
-        if (bits) un.any_odd[slot] = 1;
-        if (odd) par[p] = 0;
+          for (int d = kTok; d < kTok * C::kTpr; d <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, d);
+          if (part == 0) un.odd_v[slot][p * C::kPassTokens + ptok] = static_cast<uint8_t>(bits);
+          if (bits) un.any_odd[slot] = 1;
+        }
       }
     }
     if (it >= kSt && !__all_sync(0xffffffffu, mbar_wait(bar_empty + 8u * st, ((it / kSt) & 1) ^ 1, ab))) {
@@ -387,7 +407,7 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
       const float s = param_scale(par[p]) * unit;
       const float m = fmaf(8.f, s, param_min(par[p]) * unit);
       const uint32_t s2 = pack_f16(s, s), m2 = pack_f16(m, m);
-      const uint32_t ww[4] = {flip ? x.z : x.x, flip ? x.w : x.y, flip ? x.x : x.z, flip ? x.y : x.w};
+      const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t o[4];
@@ -396,7 +416,8 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
           const uint32_t c = codes_m8(ww[i], e);
           o[e] = kSide ? fma_f16x2(c, s2, m2) : mul_f16x2(c, s2);
         }
-        *reinterpret_cast<uint4*>(tile + place[i] + p * C::kPassTokens * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(tile + (place ^ (i << 4)) + p * C::kPassTokens * 128) =
+            make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (kSide == 0 && (GROUP == 32 || (part & 1) == 0)) {
         const int tok = p * C::kPassTokens + ptok;
@@ -411,10 +432,6 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_full + 8u * st);
-    if (it + 1 < total) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 2) : "memory");
-      post_top(it + 1);
-    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -580,60 +597,73 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
           break;
         }
         tc_fence_after();
-        uint32_t sr[2][32];
-        tmem_ld32(scol, sr[0]);
-        tmem_ld32(scol + 32, sr[1]);
         const float mult = row_scale * un.k_unit[slot];
-        const int ve = un.v_exp[slot];
-        tmem_wait_ld();
+        const bool start = w.t == w.first;
         const bool edge = key0 + kTile > k.blk.all_hi || key0 < k.blk.all_lo;
-        if (edge) {
+        float alpha = 1.f;
+        bool rescale = false;
+        // Twice in the code, with and without the masks: as one body the
+        // compiler would copy all of S between the two.
+        auto softmax = [&](auto masked) {
+          uint32_t sr[2][32];
+          tmem_ld32(scol, sr[0]);
+          tmem_ld32(scol + 32, sr[1]);
+          tmem_wait_ld();
+          if constexpr (decltype(masked)::value) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                sr[c][e] = static_cast<uint32_t>(key0 + 32 * c + e - row_lo) < seen
+                               ? sr[c][e]
+                               : __float_as_uint(-INFINITY);
+          }
+          float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              sr[c][e] = static_cast<uint32_t>(key0 + 32 * c + e - row_lo) < seen
-                             ? sr[c][e]
-                             : __float_as_uint(-INFINITY);
-          if (un.any_odd[slot])
-            for (int e = 0; e < kTile; ++e)
-              if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= un.odd_v[slot][e];
-        }
-        float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int e = 0; e < 32; e += 2)
+              mxp[(e >> 1) & 3] = max3(mxp[(e >> 1) & 3], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+          const float cand = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mult;
+          const bool up = cand > m_run + kGrow;
+          const float m_new = up ? cand : m_run;
+          alpha = up ? ex2(m_run - m_new) : 1.f;
+          rescale = up;
+          const float base = m_new == -INFINITY ? 0.f : kShift - m_new;
+          const uint64_t mult2 = f2_pack(mult, mult), base2 = f2_pack(base, base);
+          uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mxp[(e >> 1) & 3] = max3(mxp[(e >> 1) & 3], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
-        const float cand = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mult;
-        const bool start = w.t == w.first;
-        const bool up = cand > m_run + kGrow;
-        const float m_new = up ? cand : m_run;
-        const float alpha_l = up ? ex2(m_run - m_new) : 1.f;
-        const float alpha = alpha_l * ex2(static_cast<float>(v_ref - ve));  // V's unit only grows
-        const bool rescale = up || ve != v_ref;
-        const float base = m_new == -INFINITY ? 0.f : kShift - m_new;
-        const uint64_t mult2 = f2_pack(mult, mult), base2 = f2_pack(base, base);
-        uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])),
-                             mult2, base2),
-                      x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            pk[e] = pack_f16(p0, p1);
-            sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])),
+                               mult2, base2),
+                        x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              pk[e] = pack_f16(p0, p1);
+              sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
+            }
+            tmem_st16(scol + 16 * c, pk);
           }
-          tmem_st16(scol + 16 * c, pk);
+          float z0, z1;
+          f2_unpack(f2_add(sum2[0], sum2[1]), z0, z1);
+          l_run = l_run * alpha + (z0 + z1);
+          m_run = m_new;
+        };
+        if (edge)
+          softmax(std::true_type{});
+        else
+          softmax(std::false_type{});
+        if (edge && un.any_odd[slot])
+          for (int e = 0; e < kTile; ++e)
+            if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= un.odd_v[slot][e];
+        const int ve = un.v_exp[slot];
+        if (!start && ve != v_ref) {  // grown
+          alpha *= ex2(static_cast<float>(v_ref - ve));
+          rescale = true;
         }
-        float z0, z1;
-        f2_unpack(f2_add(sum2[0], sum2[1]), z0, z1);
-        l_run = l_run * alpha_l + (z0 + z1);
-        m_run = m_new;
         v_ref = ve;
         if (!start) {
           // The product of the tile before has to be complete: O may be rescaled
