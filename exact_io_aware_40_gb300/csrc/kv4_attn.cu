@@ -23,8 +23,9 @@
 // in the product, which rounds them to 2^-12 where bf16 has 2^-9, so that the
 // rounding of O to bf16 is what is left; the price is a scale.  V is taken in
 // units of 2^vexp, a power of two that grows with the largest value met (as the
-// running maximum does), P in units of 2^-kShift of the maximum's weight:
-// weights below 2^-34 of it and values below 2^-38 of the largest one are lost.
+// running maximum does) and is 1 for values of ordinary size, P in units of
+// 2^-kShift of the maximum's weight: weights below 2^-34 of it and values below
+// 2^-20 of the largest one lose bits.
 //
 // Which token is which row of the product is free as long as both products
 // agree; token_of and the swizzle of the staged 16-byte chunks (twist) are chosen
@@ -33,6 +34,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4.h"
@@ -60,7 +62,7 @@ __device__ __forceinline__ void cp_wait() {
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -69,7 +71,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // d = a b: a zero accumulator that takes no registers
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                                uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -77,7 +79,7 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -117,6 +119,11 @@ __device__ __forceinline__ uint32_t v_codes(uint32_t w, int i) {
   const uint32_t x = i < 2 ? w : w >> 8;
   if ((i & 1) == 0) return add_f16x2(and_or(x, 0x000f000fu, 0x64006400u), 0xe408e408u);  // -1032
   return fma_f16x2(and_or(x, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ bool odd_param(uint32_t p) {  // NaN or infinity in either half
   return (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
@@ -177,6 +184,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   using C = AttnCfg<HD, GROUP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scratch[kWarps + 2];
+  // The walk through the share: touched once an item, it would only take
+  // registers.  Thread 0 moves it on between two barriers.
+  __shared__ Kv4Walk<kTile> w;
+  __shared__ int4 record;
   __shared__ float stat[2][kWarps][C::kRows];
   // The merge may be launched; it waits for this grid's end by itself.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -189,12 +200,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   if (tid == 0 && u >= share.total) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (u >= share.total) return;
   bool first_item = true;
-  Kv4Walk<kTile> w;
-  w.seek(a, share, u, C::kRows);
+  if (tid == 0) {
+    w.seek(a, share, u, C::kRows);
+    record = make_int4(0, 0, 0, 0);
+  }
+  __syncthreads();
   const uint8_t* stage0 = smem + warp * C::kStages * C::kStage;
   const uint32_t stage0_u32 = smem_u32(stage0);
-  int4 record = make_int4(0, 0, 0, 0);
 
+  const float inv_scale = 1.f / a.scale_log2;
   // Lane constants of the staged layout.
   const int t0 = token_of(r);  // K, P: rows r and r + 8 are tokens t0 and t0 + 8
   const int k_at = t0 * C::kCodeRow + twist<HD>(t0) * 16 + q * 4;
@@ -208,35 +222,37 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
     v_at[e] = C::kCodes + ta[e] * C::kCodeRow + (((byte >> 4) ^ twist<HD>(ta[e])) << 4) + (byte & 15);
     vp_at[e] = 2 * C::kCodes + C::kParams + ta[e] * C::kParamRow + (r * (HD / 8)) / GROUP * 4;
   }
-  // Copies: chunk lane of a half step's codes (16 tokens), and of its params.
+  // Copies: chunk `lane` of 16 tokens' codes.
+  const long long page_bytes = static_cast<long long>(a.Hkv) * a.lay.record;
+  const int in_page = (1 << a.lay.page_shift) - 1;
   const int cp_tok = (lane * 16) / C::kCodeRow;
   const uint32_t cp_dst =
       cp_tok * C::kCodeRow + ((((lane * 16) % C::kCodeRow >> 4) ^ twist<HD>(cp_tok & 7)) << 4);
 
-  for (; u < u_end; w.next(a, C::kRows)) {
+  while (u < u_end) {
     const int first_tile = static_cast<int>(u - w.item);
     const int last_tile =
         a.whole_items ? w.blk.tiles
                       : static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
     const int tok0 = (w.blk.tile_lo + first_tile) * kTile + warp * kStepTokens;
+    const int hi = w.blk.hi, all_hi = w.blk.all_hi, all_lo = w.blk.all_lo, kv = w.req.kv;
+    const int* table = a.table + static_cast<long long>(w.b) * a.max_pages;
     // Steps of this warp that hold a key some row sees.
     const int steps =
-        min(last_tile - first_tile, max(0, (w.blk.hi - tok0 + kTile - 1) / kTile));
+        min(last_tile - first_tile, max(0, (hi - tok0 + kTile - 1) / kTile));
 
     // ------------------------------------------------ copies, kStages - 1 steps ahead
     int page = 0, page_next = 0;  // lane l: page of half l % 2 of step 16 k + l / 2
     auto fetch_page = [&](int i) -> int {
       const int tok = tok0 + (i + (lane >> 1)) * kTile + (lane & 1) * 16;
-      if (i + (lane >> 1) >= steps || tok >= w.blk.hi) return 0;
-      const int p = __ldg(a.table + static_cast<long long>(w.b) * a.max_pages +
-                          (tok >> a.lay.page_shift));
+      if (i + (lane >> 1) >= steps || tok >= hi) return 0;
+      const int p = __ldg(table + (tok >> a.lay.page_shift));
       if (p >= 0 && p < a.num_pages) return p;
       atomicCAS(a.input_err, 0, 1);
       return 0;
     };
     page_next = fetch_page(0);
     const uint8_t* head_base = a.cache + static_cast<long long>(w.h) * a.lay.record;
-    const long long page_bytes = static_cast<long long>(a.Hkv) * a.lay.record;
     auto issue = [&](int i) {
       if (i < steps) {
         if ((i & 15) == 0) {
@@ -244,34 +260,47 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
           page_next = fetch_page(i + 16);
         }
         const uint32_t dst = stage0_u32 + (i % C::kStages) * C::kStage;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int tok = tok0 + i * kTile + hf * 16;
+        const int tok = tok0 + i * kTile;
+        // `n` tokens (16 or 32) from the step's token 16 hf on, in one page.
+        auto copy = [&](int hf, auto tokens) {
+          constexpr int n = decltype(tokens)::value;
           const int pg = __shfl_sync(0xffffffffu, page, 2 * (i & 15) + hf);
-          if (hf && tok >= w.blk.hi) break;  // nothing there: left as it is, and masked
-          const int off = tok & ((1 << a.lay.page_shift) - 1);
+          const int off = (tok + hf * 16) & in_page;
           const uint8_t* rec = head_base + pg * page_bytes;
-          const uint8_t* kc = rec + off * C::kCodeRow + lane * 16;
+          const uint8_t* kc = rec + (off * C::kCodeRow + lane * 16);
           const uint8_t* vc = kc + a.lay.v_codes;
 #pragma unroll
-          for (int j = 0; j < HD / 64; ++j) {
+          for (int j = 0; j < n * C::kCodeRow / 512; ++j) {
             // 512 bytes are 16, 8 or 4 rows on; 4 rows change the twist's low bit
             const uint32_t at = dst + hf * 16 * C::kCodeRow + j * 512 +
                                 (HD == 256 && (j & 1) ? cp_dst ^ 16u : cp_dst);
             cp_async16(at, kc + j * 512);
             cp_async16(at + C::kCodes, vc + j * 512);
           }
-          constexpr int kP = C::kParamRow;  // 16-byte chunks of 16 tokens' params
-          const uint32_t pat = dst + 2 * C::kCodes + hf * 16 * kP;
-          const uint8_t* kp = rec + a.lay.k_params + off * kP;
-          const uint8_t* vp = rec + a.lay.v_params + off * kP;
-          if constexpr (kP == 32) {
-            cp_async16(pat + lane * 16, kp + lane * 16);
-            cp_async16(pat + C::kParams + lane * 16, vp + lane * 16);
-          } else if (lane < 2 * kP) {
-            const int l = lane < kP ? lane : lane - kP;
-            cp_async16(pat + (lane < kP ? 0 : C::kParams) + l * 16, (lane < kP ? kp : vp) + l * 16);
+          // K's params, then V's: chunks of 16 bytes, side by side over the lanes
+          constexpr int kChunks = n * C::kParamRow / 16;  // of either
+          const uint32_t pat = dst + 2 * C::kCodes + hf * 16 * C::kParamRow;
+          if constexpr (kChunks >= 32) {
+            const uint8_t* kp = rec + (a.lay.k_params + off * C::kParamRow + lane * 16);
+#pragma unroll
+            for (int j = 0; j < kChunks / 32; ++j) {
+              cp_async16(pat + lane * 16 + j * 512, kp + j * 512);
+              cp_async16(pat + C::kParams + lane * 16 + j * 512,
+                         kp + (a.lay.v_params - a.lay.k_params) + j * 512);
+            }
+          } else if (lane < 2 * kChunks) {
+            const bool v = lane >= kChunks;
+            const int l = (v ? lane - kChunks : lane) * 16;
+            cp_async16(pat + (v ? C::kParams : 0) + l,
+                       rec + ((v ? a.lay.v_params : a.lay.k_params) + off * C::kParamRow + l));
           }
+        };
+        if (in_page >= 31) {
+          copy(0, std::integral_constant<int, 32>{});
+        } else {
+          copy(0, std::integral_constant<int, 16>{});
+          // nothing there: left as it is, and masked
+          if (tok + 16 < hi) copy(1, std::integral_constant<int, 16>{});
         }
       }
       cp_commit();
@@ -324,6 +353,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 
     float acc[NT][HD / 16][4];
     float m_run[NT][2], l_run[NT][2];
+    float top_s[NT][2];  // scores above it move the maximum: (m_run + kGrow) / scale
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -333,6 +363,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m_run[n][e] = -INFINITY;
+        top_s[n][e] = -INFINITY;
         l_run[n][e] = 0.f;
       }
     }
@@ -350,7 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       issue(i + C::kStages - 1);
       const int tok = tok0 + i * kTile;
       const uint8_t* st = stage0 + (i % C::kStages) * C::kStage;
-      const bool edge = tok + kStepTokens > w.blk.all_hi || tok < w.blk.all_lo;
+      const bool edge = tok + kStepTokens > all_hi || tok < all_lo;
 
       // S^T of both halves
       float s[2][NT][4];
@@ -398,7 +429,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       }
       const bool upto = a.causal || a.window >= 0;
       auto visible = [&](int token, int p) {
-        bool v = token < w.req.kv;
+        bool v = token < kv;
         if (upto) v = v && token <= p;
         if (a.window >= 0) v = v && token >= p - a.window;
         return v;
@@ -432,7 +463,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int token = tok + hf * 16 + ta[e & 1] + (e & 2) * 4;
-            if (token >= w.blk.hi || odd_param(par[hf][e])) par[hf][e] = 0;
+            if (token >= hi || odd_param(par[hf][e])) par[hf][e] = 0;
           }
       }
 
@@ -448,8 +479,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          grow = grow || fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2])) *
-                                 a.scale_log2 > m_run[n][e] + kGrow;
+          grow = grow || max3(fmaxf(s[0][n][e], s[0][n][e + 2]), s[1][n][e], s[1][n][e + 2]) > top_s[n][e];
       if (__any_sync(0xffffffffu, grow)) {
         // Exponents of the largest minimum and scale of the step, numbers only.
         int em = 0, es = 0;
@@ -463,7 +493,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
             }
         em = __reduce_max_sync(0xffffffffu, em);
         es = __reduce_max_sync(0xffffffffu, es);
-        const int want = max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
+        // 1 (vexp 0) as long as it does: no param too large, the largest not small.
+        const int need = max(max(em - 127 + 1 - 14, es - 127 + 1 - 10), -110);
+        const int want = need <= 0 && need >= -20 ? 0 : need;
         float shrink = 1.f;
         if (limit == 0 || want > vexp) {
           if (limit != 0) shrink = exp2f(static_cast<float>(max(vexp - want, -126)));
@@ -486,6 +518,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
             const bool up = top > m_run[n][e] + kGrow;
             alpha[e] = up ? ex2(m_run[n][e] - top) : 1.f;
             m_run[n][e] = up ? top : m_run[n][e];
+            top_s[n][e] = (m_run[n][e] + kGrow) * inv_scale;
             l_run[n][e] *= alpha[e];
           }
 #pragma unroll
@@ -521,10 +554,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
         uint32_t sc[2], mn[2];  // scale and minimum + 8 scale of two tokens
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float sa = param_scale(par[hf][2 * k]) * v_unit, sb = param_scale(par[hf][2 * k + 1]) * v_unit;
+          const float sa = param_scale(par[hf][2 * k]), sb = param_scale(par[hf][2 * k + 1]);
           sc[k] = pack_f16(sa, sb);
-          mn[k] = pack_f16(fmaf(8.f, sa, param_min(par[hf][2 * k]) * v_unit),
-                           fmaf(8.f, sb, param_min(par[hf][2 * k + 1]) * v_unit));
+          mn[k] = pack_f16(fmaf(8.f, sa, param_min(par[hf][2 * k])),
+                           fmaf(8.f, sb, param_min(par[hf][2 * k + 1])));
+        }
+        if (vexp != 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float sa = param_scale(par[hf][2 * k]) * v_unit, sb = param_scale(par[hf][2 * k + 1]) * v_unit;
+            sc[k] = pack_f16(sa, sb);
+            mn[k] = pack_f16(fmaf(8.f, sa, param_min(par[hf][2 * k]) * v_unit),
+                             fmaf(8.f, sb, param_min(par[hf][2 * k + 1]) * v_unit));
+          }
         }
         constexpr int kWords = HD / 64;  // words of codes a lane has per token
         uint32_t v[4][kWords];
@@ -554,7 +596,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
         for (int t = 0; t < kStepTokens; ++t) {
           const uint32_t p = *reinterpret_cast<const uint32_t*>(
               st + 2 * C::kCodes + C::kParams + t * C::kParamRow + (r * (HD / 8)) / GROUP * 4);
-          if (tok + t >= w.blk.hi || !odd_param(p)) continue;
+          if (tok + t >= hi || !odd_param(p)) continue;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -571,7 +613,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
     // ------------------------------------------------ the four warps' results
     const bool whole = first_tile == 0 && last_tile == w.blk.tiles;
     const long long part_no = 2ll * blockIdx.x + (first_item && first_tile > 0 ? 0 : 1);
-    if (first_tile == 0 && !whole) record = kv4_split_record(w, share);
+    if (tid == 0 && first_tile == 0 && !whole) record = kv4_split_record(w, share);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -649,17 +691,22 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
         }
       }
     }
-    __syncthreads();  // before the next item's copies
     first_item = false;
     u = w.item + (a.whole_items ? 1 : last_tile);
+    __syncthreads();  // before the walk goes on, and before the next item's copies
+    if (u < u_end) {
+      if (tid == 0) w.next(a, C::kRows);
+      __syncthreads();
+    }
   }
   if (tid == 0) a.split[blockIdx.x] = record;
 }
 
 // Joins the parts of the items that shares' ends cut: one warp per row.  The
 // order of the sums is that of the parts, so the result does not depend on
-// which CTA ran when.
-constexpr int kMergeWarps = 4;
+// which CTA ran when.  Bound by latency: the record, the parts' statistics
+// (a lane each) and their rows (independent loads) are the three round trips.
+constexpr int kMergeWarps = 8;
 template <int HD>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     kv4_merge_kernel(const Kv4AttnArgs a, int block_rows) {
@@ -683,19 +730,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll
   for (int k = 0; k < kVec; ++k) x[k] = make_float2(0.f, 0.f);
   float l = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 st = a.part_stat[place(p)];
-    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
-    l = fmaf(st.y, f, l);
-    const float2* src = reinterpret_cast<const float2*>(a.part_o + place(p) * HD);
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const int n = min(parts - p0, 32);
+    float f = 0.f;
+    if (lane < n) {
+      const float2 st = a.part_stat[place(p0 + lane)];
+      f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+      l += st.y * f;
+    }
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+      const float g = __shfl_sync(0xffffffffu, f, p);
+      const float2* src = reinterpret_cast<const float2*>(a.part_o + place(p0 + p) * HD);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const float2 y = src[lane + 32 * k];
-      x[k].x = fmaf(y.x, f, x[k].x);
-      x[k].y = fmaf(y.y, f, x[k].y);
+      for (int k = 0; k < kVec; ++k) {
+        const float2 y = src[lane + 32 * k];
+        x[k].x = fmaf(y.x, g, x[k].x);
+        x[k].y = fmaf(y.y, g, x[k].y);
+      }
     }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const int gr = rec.y + row;
   const int t = gr / a.per_kv, head = h * a.per_kv + gr - t * a.per_kv;
   const long long o = static_cast<long long>(rec.x + t) * a.Hq + head;

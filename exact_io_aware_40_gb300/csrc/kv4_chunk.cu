@@ -444,7 +444,9 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kThreads / 32 + 2];
   __shared__ Units un;
-  __shared__ Tiles<C::kBlockRows> walks[8];  // of the converters' warps
+  // Every warp's walk through the share: touched once an item, it would only
+  // take registers.
+  __shared__ Tiles<C::kBlockRows> walks[kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t pad = ((raw_u32 + 1023u) & ~1023u) - raw_u32;
@@ -500,8 +502,15 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Abort ab{a.wait_err, abort_flag};
-  Tiles<C::kBlockRows> w;
-  w.begin(a, share);
+  Tiles<C::kBlockRows>& w = walks[warp];
+  if (lane == 0) w.begin(a, share);
+  __syncwarp();
+  auto next_item = [&]() -> bool {
+    __syncwarp();
+    int more = 0;
+    if (lane == 0) more = w.next_item(a);
+    return __shfl_sync(0xffffffffu, more, 0) != 0;  // (and the walk is the warp's again)
+  };
 
   if (warp < kConvK) {
     // ---------------------------------------------------------- rows
@@ -518,13 +527,17 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
     int it = 0;    // of this block of rows: the tiles of the items that reach it
     do {
       const auto& k = w.w;
-      const bool whole = w.first == 0 && w.last == k.blk.tiles;
-      if (w.first == 0 && !whole) record = kv4_split_record(k, share);
+      const int first_tile = w.first, last_tile = w.last;
+      const bool whole = first_tile == 0 && last_tile == k.blk.tiles;
+      if (first_tile == 0 && !whole) record = kv4_split_record(k, share);
       if (k.blk.rows <= kRows * g) {  // nothing for these rows
-        tile += w.last - w.first;
+        tile += last_tile - first_tile;
         first_item = false;
         continue;
       }
+      const int key_first = (k.blk.tile_lo + first_tile) * kTile;
+      const int key_end = (k.blk.tile_lo + last_tile) * kTile;
+      const int all_hi = k.blk.all_hi, all_lo = k.blk.all_lo;
       const bool have = kRows * g + row < k.blk.rows;
       const int gr = k.blk.row0 + (have ? kRows * g + row : 0);
       const int t = gr / a.per_kv, head = k.h * a.per_kv + gr - t * a.per_kv;
@@ -588,18 +601,17 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       float m_run = -INFINITY, l_run = 0.f;
       int v_ref = 0;
       uint32_t nan_groups = 0;
-      for (; w.t < w.last; ++w.t, ++it, ++tile) {
+      for (int key0 = key_first; key0 < key_end; key0 += kTile, ++it, ++tile) {
         const int bb = it & 1, slot = tile & (kUnits - 1);
         const uint32_t scol = tl + (bb ? 64u : 0u);
-        const int key0 = (k.blk.tile_lo + w.t) * kTile;
         if (!__all_sync(0xffffffffu, mbar_wait(bar_sfull(g, bb), (it >> 1) & 1, ab))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const float mult = row_scale * un.k_unit[slot];
-        const bool start = w.t == w.first;
-        const bool edge = key0 + kTile > k.blk.all_hi || key0 < k.blk.all_lo;
+        const bool start = key0 == key_first;
+        const bool edge = key0 + kTile > all_hi || key0 < all_lo;
         float alpha = 1.f;
         bool rescale = false;
         // Twice in the code, with and without the masks: as one body the
@@ -703,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       const float f = whole ? (l_run == 0.f ? 0.f : v_up / l_run) : v_up;
       const long long o_row = static_cast<long long>(k.req.start + t) * a.Hq + head;
       const long long p_row =
-          (2ll * blockIdx.x + (first_item && w.first > 0 ? 0 : 1)) * C::kBlockRows + kRows * g + row;
+          (2ll * blockIdx.x + (first_item && first_tile > 0 ? 0 : 1)) * C::kBlockRows + kRows * g + row;
 #pragma unroll 1
       for (int c = 0; c < HD / 16; ++c) {
         uint32_t o[16];
@@ -736,16 +748,14 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       // wait for p_full, which this warp signals after this point.
       tc_fence_before();
       first_item = false;
-    } while (w.next_item(a));
+    } while (next_item());
     if (tid == 0) a.split[blockIdx.x] = record;
   } else if (warp < kConvV) {
     regs_dec<C::kConvRegs>();
-    if (lane == 0) walks[warp - kConvK] = w;
-    convert<HD, GROUP, 0>(a, walks[warp - kConvK], smem, sb, bar_kfull, bar_kempty, un, ab);
+    convert<HD, GROUP, 0>(a, w, smem, sb, bar_kfull, bar_kempty, un, ab);
   } else if (warp < kMma) {
     regs_dec<C::kConvRegs>();
-    if (lane == 0) walks[warp - kConvK] = w;
-    convert<HD, GROUP, 1>(a, walks[warp - kConvK], smem, sb, bar_vfull, bar_vempty, un, ab);
+    convert<HD, GROUP, 1>(a, w, smem, sb, bar_vfull, bar_vempty, un, ab);
   } else {
     regs_dec<C::kMmaRegs>();
   }
@@ -786,12 +796,13 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
     };
     bool pending = false;         // is P V of the tile before still to be issued?
     do {
+      const int tiles = w.last - w.first;
       // The rows put an item's Q in place once they have read the O before, for
       // which the last product has to be issued first.
       if (pending && !issue_pv()) break;
       pending = false;
       if (w.w.blk.rows <= kRows * g) {  // nothing for these rows: the tiles are let go
-        for (; ok && w.t < w.last; ++w.t, ++tile) {
+        for (int i = 0; ok && i < tiles; ++i, ++tile) {
           const int ks = tile % C::kKSt, vs = tile % C::kVSt;
           ok = mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab);
           if (ok) mbar_arrive(bar_kempty + 8u * ks);
@@ -802,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       }
       if (!mbar_wait(bar_q(g), item & 1, ab)) break;
       ++item;
-      for (; w.t < w.last; ++w.t) {
+      for (int i = 0; i < tiles; ++i) {
         const int ks = tile % C::kKSt, bb = it & 1;
         // S over P of two tiles before: its product has to be complete.  (At an
         // item's first tile the wait for Q has shown more than that, and the
@@ -828,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
         if (pending && !issue_pv()) { ok = false; break; }
         ++it;
         ++tile;
-        prev_first = w.t == w.first;
+        prev_first = i == 0;
         pending = true;
       }
     } while (ok && w.next_item(a));

@@ -50,7 +50,11 @@ __device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req
   k.row0 = rb * block_rows;
   k.rows = min(r.n * a.per_kv - k.row0, block_rows);
   k.pos0 = r.kv - r.n;
-  const int first = k.row0 / a.per_kv, last = (k.row0 + k.rows - 1) / a.per_kv;
+  int first = 0, last = r.n - 1;
+  if (rb > 0 || k.rows < r.n * a.per_kv) {  // (one block holds all: no divisions)
+    first = k.row0 / a.per_kv;
+    last = (k.row0 + k.rows - 1) / a.per_kv;
+  }
   k.lo = 0;
   k.hi = r.kv;
   k.all_lo = 0;
@@ -80,20 +84,65 @@ __device__ __forceinline__ long long kv4_units(const Kv4AttnArgs& a, int b, int 
   return n * a.Hkv;
 }
 
+// n / d for 0 <= n, 0 < d, in 32 bits where that is enough.
+__device__ __forceinline__ long long kv4_div(long long n, long long d) {
+  if (((n | d) >> 32) == 0)
+    return static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+  return n / d;
+}
+
 struct Kv4Share {
   long long total, per;  // tiles in the list, tiles a share
   long long begin;       // first tile of the list that belongs to request b
   int b;
 };
 
-// The whole block finds its share; `scratch` holds kThreads / 32 + 2 long longs.
-// Shares are at least min_tiles long.  begin/b are set when the share is not
-// empty (blockIdx.x * per < total).
+// Every thread of the block finds the block's share; `scratch` holds
+// kThreads / 32 + 2 long longs.  Shares are at least min_tiles long.  begin/b are
+// set when the share is not empty (blockIdx.x * per < total).  Up to 128 requests
+// every warp adds up all of them by itself, which spares the barriers.
 template <int kTile, int kThreads>
 __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_rows, int min_tiles,
                                               long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
+  Kv4Share s;
+  s.b = 0;
+  s.begin = 0;
+  if (a.B <= 128) {
+    long long mine[4], sum = 0;  // requests 4 lane .. 4 lane + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 4 * lane + i;
+      mine[i] = b < a.B ? kv4_units<kTile>(a, b, block_rows, &bad) : 0;
+      sum += mine[i];
+    }
+    if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    s.total = __shfl_sync(0xffffffffu, incl, 31);
+    s.per = max(kv4_div(s.total + gridDim.x - 1, gridDim.x), static_cast<long long>(min_tiles));
+    const long long u0 = s.per * blockIdx.x;
+    if (u0 >= s.total) return s;
+    long long at = incl - sum;
+    int b = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (u0 >= at && u0 < at + mine[i]) {
+        b = 4 * lane + i;
+        s.begin = at;
+      }
+      at += mine[i];
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, b >= 0)) - 1;
+    s.b = __shfl_sync(0xffffffffu, b, who);
+    s.begin = __shfl_sync(0xffffffffu, s.begin, who);
+    return s;
+  }
   long long first = tid < a.B ? kv4_units<kTile>(a, tid, block_rows, &bad) : 0;
   long long sum = first;
   for (int b = tid + kThreads; b < a.B; b += kThreads) sum += kv4_units<kTile>(a, b, block_rows, &bad);
@@ -102,13 +151,10 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) scratch[warp] = sum;
   __syncthreads();
-  Kv4Share s;
   s.total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) s.total += scratch[w];
-  s.per = max((s.total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
-  s.b = 0;
-  s.begin = 0;
+  s.per = max(kv4_div(s.total + gridDim.x - 1, gridDim.x), static_cast<long long>(min_tiles));
   const long long u0 = s.per * blockIdx.x;
   if (u0 >= s.total) return s;
   long long run = 0;
@@ -167,7 +213,7 @@ struct Kv4Walk {
       ++rb;
       blk = kv4_block<kTile>(a, req, rb, block_rows);
     }
-    h = static_cast<int>((u - item) / blk.units);
+    h = static_cast<int>(kv4_div(u - item, blk.units));
     item += static_cast<long long>(h) * blk.units;
   }
   __device__ __forceinline__ void next(const Kv4AttnArgs& a, int block_rows) {
@@ -193,7 +239,7 @@ struct Kv4Walk {
 template <int kTile>
 __device__ __forceinline__ int4 kv4_split_record(const Kv4Walk<kTile>& w, const Kv4Share& s) {
   return make_int4(w.req.start, w.blk.row0, w.blk.rows + 512 * w.h,
-                   static_cast<int>((w.item + w.blk.units - 1) / s.per));
+                   static_cast<int>(kv4_div(w.item + w.blk.units - 1, s.per)));
 }
 
 }  // namespace fa
