@@ -106,6 +106,17 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, ui
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -759,70 +770,87 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   } else {
     regs_dec<C::kMmaRegs>();
   }
-  if (warp >= kMma && warp < kMma + C::kBlocks && lane == 0) {
+  if (warp >= kMma && warp < kMma + C::kBlocks) {
     // ---------------------------------------------------------- products
+    // The whole warp walks along and one elected lane issues: what the warp
+    // computes is the same in every lane, so the descriptors live in uniform
+    // registers, where the products take them from.
     constexpr uint32_t idS = idesc_f16(kRows, kTile, false);
     constexpr uint32_t idO = idesc_f16(kRows, HD, true);
     constexpr int kD = HD / 16, kC = kTile / 16;
-    const int g = warp - kMma;    // block of rows
+    const int g = __shfl_sync(0xffffffffu, warp - kMma, 0);  // block of rows
+    const bool leader = elect_one();
+    auto wait = [&](uint32_t bar, int parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(parity), ab)) != 0;
+    };
     bool ok = true;
     int tile = 0;                 // of the share
     int it = 0, item = 0;         // tiles and items of this block of rows
     bool prev_first = false;      // was its last tile its item's first?
-    uint64_t q0, qx;              // this block's Q
-    q0 = sdesc_sw128(sb + C::kOffQ + g * C::kQTile, 16, 1024);
-    qx = sdesc_plain(sb + C::kOffQEx + g * C::kQEx, 128, C::kExRow8);
+    const uint64_t q0 = sdesc_sw128(sb + C::kOffQ + g * C::kQTile, 16, 1024);
+    const uint64_t qx = sdesc_plain(sb + C::kOffQEx + g * C::kQEx, 128, C::kExRow8);
     const uint64_t k0 = sdesc_sw128(sb + C::kOffK, 16, 1024);
     const uint64_t kx = sdesc_plain(sb + C::kOffKEx, 128, C::kExRow8);
     const uint64_t v0 = sdesc_sw128(sb + C::kOffV, C::kAtom, 1024);
-    const uint32_t ts = tmem + 128u * g, to = tmem + C::kColO + HD * g;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t ts = tbase + 128u * g, to = tbase + C::kColO + HD * g;
     // P V of tile `tile - 1`, this block's `it - 1`.
     auto issue_pv = [&]() -> bool {
       const int vs = (tile - 1) % C::kVSt, bb = (it - 1) & 1;
-      if (!mbar_wait(bar_vfull + 8u * vs, ((tile - 1) / C::kVSt) & 1, ab)) return false;
-      if (!mbar_wait(bar_pfull(g, bb), ((it - 1) >> 1) & 1, ab)) return false;
+      if (!wait(bar_vfull + 8u * vs, ((tile - 1) / C::kVSt) & 1)) return false;
+      if (!wait(bar_pfull(g, bb), ((it - 1) >> 1) & 1)) return false;
       tc_fence_after();
-      uint64_t b[kC];
-      uint32_t p[kC];
+      if (leader) {
+        uint64_t b[kC];
+        uint32_t p[kC];
 #pragma unroll
-      for (int k = 0; k < kC; ++k) {
-        b[k] = sdesc_add(v0, vs * C::kTileBytes + k * 2048);
-        p[k] = ts + (bb ? 64u : 0u) + 8u * k;
+        for (int k = 0; k < kC; ++k) {
+          b[k] = sdesc_add(v0, vs * C::kTileBytes + k * 2048);
+          p[k] = ts + (bb ? 64u : 0u) + 8u * k;
+        }
+        mma_ts_k(to, p, b, idO, prev_first ? 0u : 1u);
+        mma_commit(bar_odone(g));
+        mma_commit(bar_vempty + 8u * vs);
       }
-      mma_ts_k(to, p, b, idO, prev_first ? 0u : 1u);
-      mma_commit(bar_odone(g));
-      mma_commit(bar_vempty + 8u * vs);
+      __syncwarp();
       return true;
     };
     bool pending = false;         // is P V of the tile before still to be issued?
     do {
       const int tiles = w.last - w.first;
+      const bool none = w.w.blk.rows <= kRows * g;
       // The rows put an item's Q in place once they have read the O before, for
       // which the last product has to be issued first.
-      if (pending && !issue_pv()) break;
+      if (pending && !issue_pv()) {
+        ok = false;
+        break;
+      }
       pending = false;
-      if (w.w.blk.rows <= kRows * g) {  // nothing for these rows: the tiles are let go
+      if (none) {  // nothing for these rows: the tiles are let go
         for (int i = 0; ok && i < tiles; ++i, ++tile) {
           const int ks = tile % C::kKSt, vs = tile % C::kVSt;
-          ok = mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab);
-          if (ok) mbar_arrive(bar_kempty + 8u * ks);
-          ok = ok && mbar_wait(bar_vfull + 8u * vs, (tile / C::kVSt) & 1, ab);
-          if (ok) mbar_arrive(bar_vempty + 8u * vs);
+          ok = wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1);
+          if (ok && leader) mbar_arrive(bar_kempty + 8u * ks);
+          ok = ok && wait(bar_vfull + 8u * vs, (tile / C::kVSt) & 1);
+          if (ok && leader) mbar_arrive(bar_vempty + 8u * vs);
         }
         continue;
       }
-      if (!mbar_wait(bar_q(g), item & 1, ab)) break;
+      if (!wait(bar_q(g), item & 1)) {
+        ok = false;
+        break;
+      }
       ++item;
       for (int i = 0; i < tiles; ++i) {
         const int ks = tile % C::kKSt, bb = it & 1;
         // S over P of two tiles before: its product has to be complete.  (At an
         // item's first tile the wait for Q has shown more than that, and the
         // phase waited for here may be over already.)
-        if (it >= 2 && pending && !mbar_wait(bar_odone(g), (it - 2) & 1, ab)) { ok = false; break; }
-        if (!mbar_wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1, ab)) { ok = false; break; }
+        if (it >= 2 && pending && !wait(bar_odone(g), (it - 2) & 1)) { ok = false; break; }
+        if (!wait(bar_kfull + 8u * ks, (tile / C::kKSt) & 1)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t dst = ts + (bb ? 64u : 0u);
-        {
+        if (leader) {
+          const uint32_t dst = ts + (bb ? 64u : 0u);
           uint64_t q[kD], b[kD];
 #pragma unroll
           for (int k = 0; k < kD; ++k) {
@@ -830,22 +858,26 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
             b[k] = sdesc_add(k0, ks * C::kTileBytes + (k >> 2) * C::kAtom + (k & 3) * 32);
           }
           mma_ss_k(dst, q, b, idS, 0u);
-        }
 #pragma unroll
-        for (int k = 0; k < C::kExSteps; ++k)
-          mma_ss(dst, sdesc_add(qx, k * 256), sdesc_add(kx, ks * C::kKEx + k * 256), idS, 1u);
-        mma_commit(bar_sfull(g, bb));
-        mma_commit(bar_kempty + 8u * ks);
+          for (int k = 0; k < C::kExSteps; ++k)
+            mma_ss(dst, sdesc_add(qx, k * 256), sdesc_add(kx, ks * C::kKEx + k * 256), idS, 1u);
+          mma_commit(bar_sfull(g, bb));
+          mma_commit(bar_kempty + 8u * ks);
+        }
+        __syncwarp();
         if (pending && !issue_pv()) { ok = false; break; }
         ++it;
         ++tile;
         prev_first = i == 0;
         pending = true;
       }
-    } while (ok && w.next_item(a));
+    } while (ok && next_item());
     if (ok && pending && *abort_flag == 0) issue_pv();
-    mma_commit(bar_drain(g));
-    mbar_wait_drain(bar_drain(g), 0);
+    if (leader) {
+      mma_commit(bar_drain(g));
+      mbar_wait_drain(bar_drain(g), 0);
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
