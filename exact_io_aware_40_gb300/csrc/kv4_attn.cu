@@ -721,44 +721,57 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   auto place = [&](int p) {  // part p: this CTA's last item, then its successors' first
     return (p == 0 ? 2ll * first + 1 : 2ll * (first + p)) * block_rows + row;
   };
-  float top = -INFINITY;
-  for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_stat[place(p)].x);
+  float2 st = make_float2(-INFINITY, 0.f);  // of part `lane`
+  if (lane < parts) st = a.part_stat[place(lane)];
+  float top = st.x;
+  for (int p = lane + 32; p < parts; p += 32) top = fmaxf(top, a.part_stat[place(p)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  constexpr int kVec = HD / 64;  // float2 a lane
-  float2 x[kVec];
+  // A row is HD / 4 float4: at d = 64 the half-warps take every other part.
+  constexpr int kSide = HD == 64 ? 2 : 1, kVec = HD == 256 ? 2 : 1;
+  const int side = HD == 64 ? lane >> 4 : 0, quad = HD == 64 ? lane & 15 : lane;
+  float4 x[kVec];
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) x[k] = make_float2(0.f, 0.f);
+  for (int k = 0; k < kVec; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
   for (int p0 = 0; p0 < parts; p0 += 32) {
     const int n = min(parts - p0, 32);
-    float f = 0.f;
-    if (lane < n) {
-      const float2 st = a.part_stat[place(p0 + lane)];
-      f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
-      l += st.y * f;
-    }
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-      const float g = __shfl_sync(0xffffffffu, f, p);
-      const float2* src = reinterpret_cast<const float2*>(a.part_o + place(p0 + p) * HD);
+    if (p0 > 0) st = lane < n ? a.part_stat[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
+    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+    l += st.y * f;
+#pragma unroll 16
+    for (int p = 0; p < n; p += kSide) {
+      const float g = __shfl_sync(0xffffffffu, f, p + side);  // 0 behind the last part
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + place(p0 + min(p + side, n - 1)) * HD);
 #pragma unroll
       for (int k = 0; k < kVec; ++k) {
-        const float2 y = src[lane + 32 * k];
-        x[k].x = fmaf(y.x, g, x[k].x);
-        x[k].y = fmaf(y.y, g, x[k].y);
+        const float4 y = src[quad + 32 * k];
+        if (p + side < n) {
+          x[k].x = fmaf(y.x, g, x[k].x);
+          x[k].y = fmaf(y.y, g, x[k].y);
+          x[k].z = fmaf(y.z, g, x[k].z);
+          x[k].w = fmaf(y.w, g, x[k].w);
+        }
       }
     }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (HD == 64) {
+    x[0].x += __shfl_xor_sync(0xffffffffu, x[0].x, 16);
+    x[0].y += __shfl_xor_sync(0xffffffffu, x[0].y, 16);
+    x[0].z += __shfl_xor_sync(0xffffffffu, x[0].z, 16);
+    x[0].w += __shfl_xor_sync(0xffffffffu, x[0].w, 16);
+  }
   const int gr = rec.y + row;
   const int t = gr / a.per_kv, head = h * a.per_kv + gr - t * a.per_kv;
   const long long o = static_cast<long long>(rec.x + t) * a.Hq + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.O) + o * (HD / 2);
+  uint2* dst = reinterpret_cast<uint2*>(a.O) + o * (HD / 4);
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) dst[lane + 32 * k] = pack_bf16(x[k].x * inv, x[k].y * inv);
+  for (int k = 0; k < kVec; ++k)
+    if (side == 0)
+      dst[quad + 32 * k] = make_uint2(pack_bf16(x[k].x * inv, x[k].y * inv), pack_bf16(x[k].z * inv, x[k].w * inv));
   if (lane == 0) a.L[o] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2f;
 }
 
@@ -812,26 +825,30 @@ cudaError_t launch_attn_rows(const Kv4AttnArgs& a, cudaStream_t stream) {
     const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
     return e != cudaSuccess ? e : launch_merge<HD>(a, ctas, block, stream);
   }
-  switch (block) {
-    case 8: return launch_attn<HD, GROUP, 1>(a, stream);
-    case 16: return launch_attn<HD, GROUP, 2>(a, stream);
-    default:
-      if constexpr (HD == 256)
-        return cudaErrorInvalidValue;
-      else
-        return launch_attn<HD, GROUP, 4>(a, stream);
-  }
+  if (block == 8) return launch_attn<HD, GROUP, 1>(a, stream);
+  if constexpr (HD <= 128)
+    if (block == 16) return launch_attn<HD, GROUP, 2>(a, stream);
+  if constexpr (HD == 64)
+    if (block == 32) return launch_attn<HD, GROUP, 4>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
+// The block of rows that serves `rows` best.  More rows in a block cost a warp
+// registers (32 at d = 128 and 16 at d = 256 spill) and products, further blocks
+// read the cache again; the kernel for many rows converts every tile once.
+// Measured, 16 requests of 8192 tokens, in us for blocks of 8, 16, 32, many:
+//   d = 64   16 rows  95  70 102 305    64 rows 347 236 198 309   128: 680 458 381 314
+//   d = 128  16 rows  83  66 157 185    48 rows 225 163 287 189    64: 293 211 291 190
+//   d = 256  16 rows  77  84   - 163    32 rows 137 140   - 166    48: 202 189   - 167
 int kv4_attn_rows(int d, int rows) {
   if (rows <= 8) return 8;
-  if (rows <= 16) return 16;
-  if (rows <= 32 && d != 256) return 32;  // d = 256: 32 rows of O would not fit the registers
-  return d == 256 ? 128 : 256;
+  if (d == 64) return rows <= 16 ? 16 : rows <= 96 ? 32 : 256;
+  if (d == 128) return rows <= 48 ? 16 : 256;
+  return rows <= 32 ? 8 : 128;
 }
 
 namespace {

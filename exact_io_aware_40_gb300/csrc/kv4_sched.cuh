@@ -110,37 +110,38 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
   s.b = 0;
   s.begin = 0;
   if (a.B <= 128) {
-    long long mine[4], sum = 0;  // requests 4 lane .. 4 lane + 3
+    long long mine[4], at[4];  // request 32 i + lane: its tiles, those before it
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int b = 4 * lane + i;
+      const int b = 32 * i + lane;
       mine[i] = b < a.B ? kv4_units<kTile>(a, b, block_rows, &bad) : 0;
-      sum += mine[i];
     }
     if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
-    long long incl = sum;
+    s.total = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
+    for (int i = 0; i < 4; ++i) {
+      if (32 * i >= a.B) break;
+      long long incl = mine[i];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      at[i] = s.total + incl - mine[i];
+      s.total += __shfl_sync(0xffffffffu, incl, 31);
     }
-    s.total = __shfl_sync(0xffffffffu, incl, 31);
     s.per = max(kv4_div(s.total + gridDim.x - 1, gridDim.x), static_cast<long long>(min_tiles));
     const long long u0 = s.per * blockIdx.x;
     if (u0 >= s.total) return s;
-    long long at = incl - sum;
-    int b = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (u0 >= at && u0 < at + mine[i]) {
-        b = 4 * lane + i;
-        s.begin = at;
+      if (32 * i >= a.B) break;
+      const uint32_t who = __ballot_sync(0xffffffffu, u0 >= at[i] && u0 < at[i] + mine[i]);
+      if (who) {
+        s.b = 32 * i + __ffs(who) - 1;
+        s.begin = __shfl_sync(0xffffffffu, at[i], __ffs(who) - 1);
       }
-      at += mine[i];
     }
-    const int who = __ffs(__ballot_sync(0xffffffffu, b >= 0)) - 1;
-    s.b = __shfl_sync(0xffffffffu, b, who);
-    s.begin = __shfl_sync(0xffffffffu, s.begin, who);
     return s;
   }
   long long first = tid < a.B ? kv4_units<kTile>(a, tid, block_rows, &bad) : 0;
