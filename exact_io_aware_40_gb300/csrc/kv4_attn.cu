@@ -169,7 +169,8 @@ struct AttnCfg {
   static constexpr int kCodes = kStepTokens * kCodeRow, kParams = kStepTokens * kParamRow;
   static constexpr int kStage = 2 * (kCodes + kParams);  // bytes: K codes, V codes, K, V params
   static_assert(kStage % 128 == 0, "the swizzle works on addresses");
-  static constexpr int kStages = HD == 64 ? 4 : HD == 128 ? (NT == 4 ? 4 : 2) : 2;
+  // As many as the resident CTAs leave room for.
+  static constexpr int kStages = HD == 64 ? 4 : HD == 128 && (NT > 1 || GROUP == 64) ? 3 : 2;
   static constexpr int kStageBytes = kWarps * kStages * kStage;
   static constexpr int kMergeBytes = kWarps * 8 * HD * 4;  // 8 rows of every warp's O
   static constexpr int kSmem = kStageBytes > kMergeBytes ? kStageBytes : kMergeBytes;
@@ -246,7 +247,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
     auto fetch_page = [&](int i) -> int {
       const int tok = tok0 + (i + (lane >> 1)) * kTile + (lane & 1) * 16;
       if (i + (lane >> 1) >= steps || tok >= hi) return 0;
-      const int p = __ldg(table + (tok >> a.lay.page_shift));
+      int p;  // volatile: issued here, long before it is used
+      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(p) : "l"(table + (tok >> a.lay.page_shift)));
+      return p;
+    };
+    auto valid_page = [&](int p) -> int {
       if (p >= 0 && p < a.num_pages) return p;
       atomicCAS(a.input_err, 0, 1);
       return 0;
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
     auto issue = [&](int i) {
       if (i < steps) {
         if ((i & 15) == 0) {
-          page = page_next;
+          page = valid_page(page_next);
           page_next = fetch_page(i + 16);
         }
         const uint32_t dst = stage0_u32 + (i % C::kStages) * C::kStage;
@@ -305,13 +310,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       }
       cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
-
-    // ------------------------------------------------ this block's queries
+    // This block's queries: loaded while the first pages are looked up.
     uint32_t qf[NT][HD / 32][4];       // B fragments of Q^T
-    float qsum[NT][C::kGroups][2];     // sums of Q over a group, rows 2 q, 2 q + 1
-    int pos[NT][2];                    // position of rows 2 q, 2 q + 1 (-1: no such row)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = 8 * n + r;
@@ -320,17 +320,28 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       const int t = gr / a.per_kv, head = w.h * a.per_kv + gr - t * a.per_kv;
       const uint16_t* src = a.Q + static_cast<long long>(w.req.start + t) * a.q_ts +
                             static_cast<long long>(head) * a.q_hs + 8 * q;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        qf[n][c][0] = qf[n][c][1] = qf[n][c][2] = qf[n][c][3] = 0;
+        if (have)  // volatile: issued here
+          asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(qf[n][c][0]), "=r"(qf[n][c][1]), "=r"(qf[n][c][2]), "=r"(qf[n][c][3])
+                       : "l"(src + 32 * c));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+
+    // ------------------------------------------------ sums over the queries' groups
+    float qsum[NT][C::kGroups][2];     // rows 2 q, 2 q + 1
+    int pos[NT][2];                    // position of rows 2 q, 2 q + 1 (-1: no such row)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       float part[C::kGroups];
 #pragma unroll
       for (int g = 0; g < C::kGroups; ++g) part[g] = 0.f;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (have) x = __ldg(reinterpret_cast<const uint4*>(src + 32 * c));
-        qf[n][c][0] = x.x;
-        qf[n][c][1] = x.y;
-        qf[n][c][2] = x.z;
-        qf[n][c][3] = x.w;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           part[32 * c / GROUP] += __uint_as_float(qf[n][c][i] << 16) +
