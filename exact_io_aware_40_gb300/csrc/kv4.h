@@ -79,6 +79,7 @@ struct Kv4AttnArgs {
   float scale_log2;  // scale * log2(e)
   int causal, window;
   int whole_items;   // items are not cut (kv4_sched.cuh)
+  int lead;          // places an item takes in the list beside its tiles' (set by the launcher)
   int *wait_err, *input_err;
   // workspace: one Kv4Split per CTA, then per CTA two partial results of
   // `rows` query rows: statistics (m, l) and fp32 O

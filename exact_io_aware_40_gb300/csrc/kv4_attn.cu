@@ -48,6 +48,7 @@ constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kStepTokens = 32;
 constexpr int kTile = kWarps * kStepTokens;  // one step of every warp
+constexpr int kLead = 2;        // tiles that a change of items costs
 constexpr float kGrow = 4.f;    // log2 units: m moves only when the maximum passes it by more
 constexpr float kShift = 10.f;  // P is at most 2^(kGrow + kShift)
 constexpr float kLn2f = 0.693147180559945309f;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q = lane & 3;  // row / column pair of the product's fragments
 
-  const Kv4Share share = kv4_share<kTile, kAttnThreads>(a, C::kRows, 1, scratch);
+  const Kv4Share share = kv4_share<kTile, kAttnThreads>(a, C::kRows, a.whole_items ? 1 : kLead + 1, scratch);
   long long u = share.per * blockIdx.x;
   const long long u_end = min(share.total, u + share.per);
   if (tid == 0 && u >= share.total) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -231,10 +232,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       cp_tok * C::kCodeRow + ((((lane * 16) % C::kCodeRow >> 4) ^ twist<HD>(cp_tok & 7)) << 4);
 
   while (u < u_end) {
-    const int first_tile = static_cast<int>(u - w.item);
-    const int last_tile =
-        a.whole_items ? w.blk.tiles
-                      : static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
+    int first_tile, last_tile;
+    const long long u_next = kv4_part(a, w, u, u_end, &first_tile, &last_tile);
+    if (first_tile >= last_tile) break;  // the share ends before the item's tiles
     const int tok0 = (w.blk.tile_lo + first_tile) * kTile + warp * kStepTokens;
     const int hi = w.blk.hi, all_hi = w.blk.all_hi, all_lo = w.blk.all_lo, kv = w.req.kv;
     const int* table = a.table + static_cast<long long>(w.b) * a.max_pages;
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       }
     }
     first_item = false;
-    u = w.item + (a.whole_items ? 1 : last_tile);
+    u = u_next;
     __syncthreads();  // before the walk goes on, and before the next item's copies
     if (u < u_end) {
       if (tid == 0) w.next(a, C::kRows);
@@ -822,7 +822,9 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
   const int ctas = per_sm * sms < kKv4MaxCtas ? per_sm * sms : kKv4MaxCtas;
-  kv4_attn_kernel<HD, GROUP, NT><<<ctas, kAttnThreads, C::kSmem, stream>>>(a);
+  Kv4AttnArgs ag = a;
+  ag.lead = kLead;
+  kv4_attn_kernel<HD, GROUP, NT><<<ctas, kAttnThreads, C::kSmem, stream>>>(ag);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.whole_items) return e;
   return launch_merge<HD>(a, ctas, C::kRows, stream);

@@ -34,7 +34,6 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "kernels.h"
 #include "kv4.h"
@@ -46,6 +45,7 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a warpgroup
 constexpr int kTile = 64;
+constexpr int kLead = 2;    // tiles that a change of items costs
 constexpr float kGrow = 4.f;
 constexpr float kShift = 10.f;
 constexpr float kLn2f = 0.693147180559945309f;
@@ -190,26 +190,26 @@ __device__ __forceinline__ bool bar_and_128(int id, bool pred) {
 template <int kBlockRows>
 struct Tiles {
   Kv4Walk<kTile> w;
-  long long u, u_end;
+  long long u, u_next, u_end;
   int t, first, last;  // tile of the item; the part of it in this share
 
   __device__ __forceinline__ void begin(const Kv4AttnArgs& a, const Kv4Share& s) {
     u = s.per * blockIdx.x;
     u_end = min(s.total, u + s.per);
     w.seek(a, s, u, kBlockRows);
-    open();
+    open(a);
   }
-  __device__ __forceinline__ void open() {
-    t = first = static_cast<int>(u - w.item);
-    last = static_cast<int>(min(static_cast<long long>(w.blk.tiles), u_end - w.item));
+  __device__ __forceinline__ void open(const Kv4AttnArgs& a) {
+    u_next = kv4_part(a, w, u, u_end, &first, &last);
+    t = first;
   }
-  // To the next item; false behind the share's end.
+  // To the next item with tiles in this share; false if there is none.
   __device__ __forceinline__ bool next_item(const Kv4AttnArgs& a) {
-    u = w.item + last;
+    u = u_next;
     if (u >= u_end) return false;
     w.next(a, kBlockRows);
-    open();
-    return true;
+    open(a);
+    return first < last;
   }
 };
 
@@ -253,7 +253,6 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   const int ptok = cw * (32 / C::kTpr) + lane / (kTok * C::kTpr) * kTok + lane % kTok;
   const int group = part * 32 / GROUP;
   __syncwarp();
-  const int total = static_cast<int>(walk.u_end - walk.u);
   const long long page_bytes = static_cast<long long>(a.Hkv) * a.lay.record;
   const int shift = a.lay.page_shift, in_page = (1 << shift) - 1;
   // This thread's place in the ring: codes of pass p of tile n, then params.
@@ -291,8 +290,10 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
       if (tok < hi) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(pages[p]) : "l"(table + (tok >> shift)));
     }
   };
-  auto copy = [&](int n) {
-    if (n < total) {
+  int n = 0;         // tiles copied
+  bool more = true;  // is there another one?
+  auto copy = [&]() {
+    if (more) {
       if (ct == 0)
         un.meta[kSide][n & 7] = (key + kTile > all_hi || key < all_lo ? 1 : 0) | (opening ? 2 : 0);
 #pragma unroll
@@ -312,11 +313,15 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
       }
       opening = false;
       key += kTile;
-      if (key >= key_end && n + 1 < total) {
-        if (lane == 0) walk.next_item(a);
-        open();
+      ++n;
+      if (key >= key_end) {
+        __syncwarp();
+        int on = 0;
+        if (lane == 0) on = walk.next_item(a);
+        more = __shfl_sync(0xffffffffu, on, 0) != 0;
+        if (more) open();
       }
-      if (n + 1 < total) locate();
+      if (more) locate();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -347,10 +352,10 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   bool ok = true;
   open();
   locate();
-  for (int n = 0; n < C::kRing - 1; ++n) copy(n);
-  for (int it = 0; it < total; ++it) {
+  for (int i = 0; i < C::kRing - 1; ++i) copy();
+  for (int it = 0; it < n; ++it) {
     const int st = it % kSt, slot = it & (kUnits - 1);
-    copy(it + C::kRing - 1);
+    copy();
     asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 1) : "memory");
     uint32_t par[C::kPasses], par_v[C::kPasses];
     uint32_t top = 0, top_v = 0;
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const Kv4Share share = kv4_share<kTile, kThreads>(a, C::kBlockRows, 4, scratch);
+  const Kv4Share share = kv4_share<kTile, kThreads>(a, C::kBlockRows, kLead + 2, scratch);
   if (share.per * blockIdx.x >= share.total) {
     if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
@@ -625,14 +630,12 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
         const bool edge = key0 + kTile > all_hi || key0 < all_lo;
         float alpha = 1.f;
         bool rescale = false;
-        // Twice in the code, with and without the masks: as one body the
-        // compiler would copy all of S between the two.
-        auto softmax = [&](auto masked) {
+        {
           uint32_t sr[2][32];
           tmem_ld32(scol, sr[0]);
           tmem_ld32(scol + 32, sr[1]);
           tmem_wait_ld();
-          if constexpr (decltype(masked)::value) {
+          if (edge) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -674,11 +677,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
           f2_unpack(f2_add(sum2[0], sum2[1]), z0, z1);
           l_run = l_run * alpha + (z0 + z1);
           m_run = m_new;
-        };
-        if (edge)
-          softmax(std::true_type{});
-        else
-          softmax(std::false_type{});
+        }
         if (edge && un.any_odd[slot])
           for (int e = 0; e < kTile; ++e)
             if (static_cast<uint32_t>(key0 + e - row_lo) < seen) nan_groups |= un.odd_v[slot][e];
@@ -904,7 +903,9 @@ cudaError_t launch_chunk(const Kv4AttnArgs& a, cudaStream_t stream, int* ctas) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
   *ctas = sms < kKv4MaxChunkCtas ? sms : kKv4MaxChunkCtas;
-  kv4_chunk_kernel<HD, GROUP><<<*ctas, C::kThreads, C::kSmem, stream>>>(a);
+  Kv4AttnArgs ag = a;
+  ag.lead = kLead;
+  kv4_chunk_kernel<HD, GROUP><<<*ctas, C::kThreads, C::kSmem, stream>>>(ag);
   return cudaGetLastError();
 }
 

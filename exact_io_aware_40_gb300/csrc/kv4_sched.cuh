@@ -7,7 +7,9 @@
 // kTile-token tiles, those that hold a key visible to one of its rows (at least
 // one, so that a block that sees nothing still writes its zeros).  All tiles of
 // all items form one list which is cut into equal shares, one per CTA: lengths
-// may differ by any factor and the shares do not.  An item that a share's end
+// may differ by any factor and the shares do not.  Changing from one item to the
+// next costs a CTA about as much as some tiles (its results, the first copies),
+// so an item's tiles are led in the list by `lead` places that stand for that.  An item that a share's end
 // cuts is finished from partial results by a second kernel.  Where no item is
 // long (whole_items) a place in the list is an item instead, and that kernel is
 // not needed.
@@ -40,7 +42,7 @@ struct Kv4Block {
   int lo, hi;             // keys that some row sees
   int all_lo, all_hi;     // keys that every row sees
   int tile_lo, tiles;
-  int units;              // places in the list: tiles, or 1 if items are not cut
+  int units;              // places in the list: a.lead + tiles, or 1 if items are not cut
 };
 
 template <int kTile>
@@ -70,7 +72,7 @@ __device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req
   }
   k.tile_lo = k.lo / kTile;
   k.tiles = max((k.hi + kTile - 1) / kTile - k.tile_lo, 1);
-  k.units = a.whole_items ? 1 : k.tiles;
+  k.units = a.whole_items ? 1 : a.lead + k.tiles;
   return k;
 }
 
@@ -92,8 +94,8 @@ __device__ __forceinline__ long long kv4_div(long long n, long long d) {
 }
 
 struct Kv4Share {
-  long long total, per;  // tiles in the list, tiles a share
-  long long begin;       // first tile of the list that belongs to request b
+  long long total, per;  // places in the list, and in a share
+  long long begin;       // first place that belongs to request b
   int b;
 };
 
@@ -193,7 +195,7 @@ struct Kv4Walk {
   Kv4Req req;
   Kv4Block blk;
   int b, rb, h, blocks;
-  long long item;  // index in the list of the item's first tile
+  long long item;  // the item's first place in the list
 
   __device__ __forceinline__ void open(const Kv4AttnArgs& a, int block_rows) {
     bool bad = false;
@@ -203,7 +205,7 @@ struct Kv4Walk {
     h = 0;
     if (blocks) blk = kv4_block<kTile>(a, req, 0, block_rows);
   }
-  // To the item that holds tile u of the list, from the request that holds it.
+  // To the item that holds place u of the list, from the request that holds it.
   __device__ __forceinline__ void seek(const Kv4AttnArgs& a, const Kv4Share& s, long long u,
                                        int block_rows) {
     b = s.b;
@@ -231,6 +233,23 @@ struct Kv4Walk {
     }
   }
 };
+
+// The tiles [first, last) of the walk's item that places [u, u_end) of the list
+// stand for, none if the share ends within its lead; returns the place behind
+// them.
+template <int kTile>
+__device__ __forceinline__ long long kv4_part(const Kv4AttnArgs& a, const Kv4Walk<kTile>& w, long long u,
+                                              long long u_end, int* first, int* last) {
+  if (a.whole_items) {
+    *first = 0;
+    *last = w.blk.tiles;
+    return w.item + 1;
+  }
+  const int end = static_cast<int>(min(static_cast<long long>(w.blk.units), u_end - w.item));
+  *first = max(static_cast<int>(u - w.item) - a.lead, 0);
+  *last = max(end - a.lead, 0);
+  return w.item + end;
+}
 
 // The record a CTA leaves for the merge: the item, cut by this share's end,
 // that begins in it (x: first query of its request, y: first row of its block,
