@@ -12,6 +12,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kMaxTokens = 1 << 30;  // token numbers stay within int
+
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 bool page_ok(int page_size) {
@@ -54,7 +56,7 @@ fa_status fa_kv4_plan(const int32_t* past_len, const int32_t* new_len, int B, in
   if (!page_ok(page_size) || B > FA_KV4_MAX_BATCH) return FA_ERR_UNSUPPORTED;
   // Slots, ring positions and token counts stay within int.
   if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL || num_pages > (1 << 30) ||
-      static_cast<long long>(max_pages) * page_size > 0x7fffffffLL || max_tokens > (1 << 30))
+      static_cast<long long>(max_pages) * page_size > 0x7fffffffLL || max_tokens > kMaxTokens)
     return FA_ERR_UNSUPPORTED;
   const void* words[] = {past_len, new_len, block_table, free_list, free_state,
                          kv_len,   cu_q,    slots,       state_out};
@@ -89,6 +91,7 @@ fa_status fa_kv4_append(const void* K, const void* V, int T, int Hkv, int d, int
   if (!K || !V || !slots || !cache || T < 1) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(num_pages, page_size, d, group, Hkv);
   if (st != FA_OK) return st;
+  if (T > kMaxTokens) return FA_ERR_UNSUPPORTED;
   if (!strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride) ||
       !aligned(K, 16) || !aligned(V, 16) || !aligned(cache, 16) || !aligned(slots, 4))
     return FA_ERR_INVALID_ARG;
@@ -119,6 +122,7 @@ fa_status fa_kv4_gather(const int32_t* slots, const void* cache, int num_pages, 
   if (!K || !V || !slots || !cache || T < 1) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(num_pages, page_size, d, group, Hkv);
   if (st != FA_OK) return st;
+  if (T > kMaxTokens) return FA_ERR_UNSUPPORTED;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cache, 16) || !aligned(slots, 4))
     return FA_ERR_INVALID_ARG;
   fa::ErrorWords err;
@@ -160,7 +164,7 @@ fa_status fa_kv4_attn(const void* Q, const void* cache, const int32_t* block_tab
   if (st != FA_OK) return st;
   if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   // Positions and row numbers stay within int.
-  if (static_cast<long long>(max_pages) * page_size > 0x3fffffffLL ||
+  if (static_cast<long long>(max_pages) * page_size > 0x3fffffffLL || total_q > kMaxTokens ||
       static_cast<long long>(max_q) * (Hq / Hkv) > 0x3fffffffLL)
     return FA_ERR_UNSUPPORTED;
   if (!strides_ok(q_token_stride, q_head_stride) || !aligned(Q, 16) || !aligned(O, 16) ||

@@ -44,13 +44,14 @@ def test_plan_refuses(lib, bad, status):
 @pytest.mark.parametrize("bad,status", [
     (dict(K=NULL), 1), (dict(K=ODD), 1), (dict(V=ODD), 1), (dict(cache=ODD), 1), (dict(T=0), 1), (dict(H=0), 1),
     (dict(kt=516), 1), (dict(vh=-128), 1), (dict(d=96), 2), (dict(group=128), 2), (dict(page=8), 2),
-    (dict(pages=0), 1), (dict(pages=1 << 28), 2), (dict(H=65536), 2)])
+    (dict(pages=0), 1), (dict(pages=1 << 28), 2), (dict(H=65536), 2), (dict(T=(1 << 30) + 1), 2)])
 def test_append_refuses(lib, bad, status):
     assert call(lib.fa_kv4_append, APPEND, **bad) == status
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(K=NULL), 1), (dict(V=ODD), 1), (dict(slots=NULL), 1), (dict(T=0), 1), (dict(d=32), 2), (dict(group=16), 2)])
+    (dict(K=NULL), 1), (dict(V=ODD), 1), (dict(slots=NULL), 1), (dict(T=0), 1), (dict(d=32), 2), (dict(group=16), 2),
+    (dict(T=(1 << 30) + 1), 2)])
 def test_gather_refuses(lib, bad, status):
     assert call(lib.fa_kv4_gather, GATHER, **bad) == status
 
@@ -60,7 +61,7 @@ def test_gather_refuses(lib, bad, status):
     (dict(bytes=64), 1), (dict(B=0), 1), (dict(total=0), 1), (dict(max_q=0), 1), (dict(Hq=7), 1),
     (dict(Hq=0), 1), (dict(d=80), 2), (dict(qt=12), 1), (dict(qh=-8), 1), (dict(window=-2), 1),
     (dict(scale=ctypes.c_float(0.0)), 1), (dict(scale=ctypes.c_float(float("nan"))), 1), (dict(width=0), 1),
-    (dict(width=1 << 27), 2), (dict(max_q=1 << 29), 2), (dict(page=48), 2)])
+    (dict(width=1 << 27), 2), (dict(max_q=1 << 29), 2), (dict(page=48), 2), (dict(total=(1 << 30) + 1), 2)])
 def test_attention_refuses(lib, bad, status):
     assert call(lib.fa_kv4_attn, ATTN, **bad) == status
 

@@ -274,7 +274,7 @@ def compare(o, l, c, rows=None):
     worst = (np.abs(o - O)[f] / (tol_o[f] + 1e-30)).max() if f.any() else 0.0
     assert worst <= 1.0, "O off by %.3g of its bound" % worst
     f = np.isfinite(L)
-    worst = (np.abs(l - L)[f] / tol_l[f]).max() if f.any() else 0.0
+    worst = (np.abs(l[f] - L[f]) / tol_l[f]).max() if f.any() else 0.0
     assert worst <= 1.0, "L off by %.3g of its bound" % worst
     assert (o[np.isneginf(l)] == 0).all()
 
@@ -363,11 +363,10 @@ def test_attention_ignores_what_was_never_written(fa, nq, d):
     check(fa, c)
 
 
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("per", [1, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("per", [1, 2, 8, 14])
 def test_attention_values_that_are_not_numbers(fa, d, per):
     # the newest tokens hold NaN in some groups: only the rows that see them take it
-    import torch
     c = attention_case(41, [90], [9], 1, per, d, 32, 16)
     for which, token in ((1, 85), (1, 89), (0, 88)):
         slot = int(c["table"][0, token // 16]) * 16 + token % 16
@@ -423,6 +422,135 @@ def test_attention_reports_pages_and_offsets_out_of_range(fa):
     long = dict(c, kv_len=np.asarray([100, 1 << 30], np.int32))
     long["table"] = np.where(long["table"] < 0, 0, long["table"])
     check(fa, long)
+
+
+@pytest.mark.parametrize("nq", [1, 30])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_queries_that_are_not_numbers(fa, nq, d):
+    # a query's NaN or infinity stays in its own row
+    import torch
+    c = attention_case(43, [300, 70], [nq, nq], 2, 4, d, 32, 32)
+    clean, _ = run_attention(fa, c)
+    q = dev_bf16(R.bf16_bits(c["q"]))
+    q[0, 1, 3], q[-1, 5, 7] = float("nan"), float("inf")
+    args = [dev(c[x]) for x in ("cache", "table", "cu", "kv_len")]
+    o, l = fa.kv4_attention(q, *args, nq, 32, 32)
+    fa.fa_check_error()
+    hit = torch.zeros(o.shape[:2], dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[-1, 5] = True
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(l[0, 1])
+    assert torch.equal(o[~hit], clean[~hit]) and not torch.isnan(l[~hit]).any()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sizes", [(2.0 ** -40, 0), (2.0 ** 40, 0), (2.0 ** -12, 1 / 24), (2.0 ** 12, -1 / 24)])
+def test_attention_of_keys_and_values_of_any_size(fa, nq, d, sizes):
+    # far from 1, and growing or shrinking along the tokens (the kernels' fp16 units follow)
+    base, slope = sizes
+    c = attention_case(17, [333], [nq], 1, 2, d, 32, 16)
+    page = 16
+    sec = R.sections(page, d, 32)
+    place = np.zeros(c["cache"].shape[0])
+    place[c["table"][0, :21]] = np.arange(21)
+    grow = base * 2.0 ** (slope * (place[:, None] * page + np.arange(page)))
+    for which, (lo, hi) in ((0, sec[1]), (1, sec[3])):
+        par = np.ascontiguousarray(c["cache"][..., lo:hi]).view(np.uint16)
+        v = R.bf16_value(par).reshape(par.shape[0], 1, page, -1) * grow[:, None, :, None]
+        c["cache"][..., lo:hi] = R.bf16_bits(v).reshape(par.shape).view(np.uint8)
+    c["q"] = R.bf16_value(R.bf16_bits(c["q"] / base))   # scores of ordinary size
+    check(fa, c)
+
+
+@pytest.mark.parametrize("B,nq", [(129, 1), (300, 1), (200, 9), (1100, 1)])
+def test_attention_of_many_requests(fa, B, nq):
+    # more requests than a warp adds up, several to a share, some without queries or keys
+    rng = np.random.default_rng(B)
+    n = [int(x) for x in rng.integers(0, nq + 1, B)]
+    lens = [int(x) if rng.random() < 0.95 else 0 for x in rng.integers(1, 150, B)]
+    lens[B // 2] = 1500
+    n[0] = nq
+    check(fa, attention_case(B, lens, n, 1, 4, 64, 32, 16))
+    check(fa, attention_case(B + 1, lens, n, 1, 8, 128, 64, 64))
+
+
+@pytest.mark.parametrize("nq", [1, 12, 100])
+def test_attention_is_bitwise_repeatable(fa, nq):
+    import torch
+    c = attention_case(63, [9000, 700, 1], [nq, min(nq, 5), 1], 2, 4, 128, 32, 64)
+    first = run_attention(fa, c)
+    for _ in range(3):
+        for a, b in zip(first, run_attention(fa, c)):
+            assert torch.equal(a, b)
+    fa.fa_check_error()
+
+
+def test_offsets_past_32_bits(fa):
+    # a cache of more than 2^32 bytes: its last pages are written, read and attended to
+    import torch
+    heads, d, page = 16, 128, 128
+    record = fa.kv4_page_bytes(d, page, 32)
+    pages = (1 << 32) // (heads * record) + 40
+    cache = fa.kv4_cache(pages, heads, page, d)
+    assert cache.numel() > 1 << 32
+    T = 200
+    rng = np.random.default_rng(5)
+    kb, vb = (R.bf16_bits(rng.standard_normal((T, heads, d))) for _ in range(2))
+    ids = np.array([pages - 1, pages - 3], np.int32)
+    j = np.arange(T)
+    slots = ids[j // page].astype(np.int64) * page + j % page
+    fa.kv4_append(dev_bf16(kb), dev_bf16(vb), i32(slots), cache, page)
+    k, v = fa.kv4_gather(i32(slots), cache, page, d)
+    fa.fa_check_error()
+    for x, bits in ((k, kb), (v, vb)):
+        want = dev(R.values(*R.quantise(R.bf16_value(bits), 32), 32)).float().bfloat16()
+        assert (x == want).all()
+    small = np.zeros((2, heads, record), np.uint8)
+    small[:] = cache[[pages - 1, pages - 3]].cpu().numpy()
+    for nq in (1, 60):
+        q = R.bf16_value(R.bf16_bits(rng.standard_normal((nq, heads, d))))
+        c = dict(q=q, cache=small, table=np.array([[0, 1]], np.int32), cu=np.array([0, nq], np.int32),
+                 kv_len=np.array([T], np.int32), page=page, group=32, scale=1 / np.sqrt(d), causal=True, window=-1)
+        o, l = fa.kv4_attention(dev_bf16(R.bf16_bits(q)), cache, dev(ids[None]), dev(c["cu"]), dev(c["kv_len"]), nq,
+                                page, 32)
+        fa.fa_check_error()
+        compare(o, l, c)
+
+
+def test_the_binding_refuses(fa):
+    import torch
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    n32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    cache = torch.zeros(4, 2, fa.kv4_page_bytes(64, 16), dtype=torch.uint8, device="cuda")
+    k = bf(8, 2, 64)
+    good = dict(k=k, v=k, slots=n32(8), cache=cache, page_size=16)
+    for bad in (dict(k=bf(8, 3, 64), v=bf(8, 3, 64)), dict(v=bf(7, 2, 64)), dict(k=k.float()), dict(slots=n32(9)),
+                dict(slots=n32(8).long()), dict(cache=cache[:, :, :-16].contiguous()), dict(cache=cache.transpose(0, 1)),
+                dict(k=bf(8, 2, 68)[:, :, :64]), dict(k=bf(8, 2, 128)[:, :, ::2]), dict(k=bf(8, 2, 80)[:, :, 4:68]),
+                dict(page_size=32), dict(k=k[0]), dict(v=k.cpu())):
+        with pytest.raises(ValueError):
+            fa.kv4_append(**dict(good, **bad))
+    q = bf(3, 4, 64)
+    good = dict(q=q, cache=cache, block_table=n32(3, 2), cu_q=n32(4), kv_len=n32(3), max_q=1, page_size=16)
+    for bad in (dict(q=bf(3, 5, 64)), dict(cu_q=n32(3)), dict(kv_len=n32(4)), dict(max_q=0), dict(window=-2),
+                dict(block_table=n32(6)), dict(block_table=n32(2, 3).T), dict(out=bf(3, 4, 128)), dict(lse=bf(3, 4)),
+                dict(group=64), dict(q=q.cpu()), dict(max_q=1 << 32), dict(workspace=n32(4))):
+        with pytest.raises(ValueError):
+            fa.kv4_attention(**dict(good, **bad))
+    with pytest.raises(fa.FAError):
+        fa.kv4_attention(**dict(good, scale=0.0))
+    with pytest.raises(fa.FAError):
+        fa.kv4_attention(**dict(good, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")))
+    for bad in (dict(new_len=n32(4)), dict(free_state=n32(1)), dict(block_table=n32(3)), dict(max_tokens=0),
+                dict(free_list=n32(9)[::2]), dict(past_len=n32(3).long())):
+        with pytest.raises(ValueError):
+            fa.kv4_plan(**dict(dict(past_len=n32(3), new_len=n32(3), block_table=n32(3, 2), free_list=n32(9),
+                                    free_state=n32(2), page_size=16, max_tokens=4), **bad))
+    # nothing to do is not an error
+    fa.kv4_append(bf(0, 2, 64), bf(0, 2, 64), n32(0), cache, 16)
+    assert fa.kv4_gather(n32(0), cache, 16, 64)[0].shape == (0, 2, 64)
+    assert fa.kv4_attention(bf(0, 4, 64), cache, n32(3, 2), n32(4), n32(3), 1, 16)[1].shape == (0, 4)
+    fa.fa_check_error()
 
 
 # ------------------------------------------------------------------ together
@@ -544,6 +672,32 @@ def test_captured_step_replays(fa):
             want = p @ V[:, h // per]
             tol = 2.0 ** -8 * (3.1 * p @ np.abs(V[:, h // per]) + np.abs(want)) + 1e-4
             assert (np.abs(o[b, h] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("nq", [9, 60])
+def test_captured_attention_replays(fa, nq):
+    # two graphs with buffers of their own, replayed in turn on changing inputs
+    import torch
+    cases = [attention_case(95 + i, [900, 64], [nq, nq], 2, 4, 128, 32, 64) for i in range(2)]
+    args = [(dev_bf16(R.bf16_bits(c["q"])), dev(c["cache"]), dev(c["table"]), dev(c["cu"]), dev(c["kv_len"]))
+            for c in cases]
+    alone = [fa.kv4_attention(*a, nq, 64) for a in args]
+    graphs, outs = [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fa.kv4_attention(*a, nq, 64))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        for o in outs[i]:
+            o.zero_()
+        graphs[i].replay()
+        for o, w in zip(outs[i], alone[i]):
+            assert torch.equal(o, w)
+    args[0][4].copy_(i32([500, 63]))     # other lengths
+    graphs[0].replay()
+    compare(*outs[0], dict(cases[0], kv_len=np.array([500, 63], np.int32)))
+    fa.fa_check_error()
 
 
 def test_two_streams_with_workspaces_of_their_own(fa):
