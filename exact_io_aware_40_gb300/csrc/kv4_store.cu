@@ -11,8 +11,8 @@
 // (Markstein's method).  The other groups, and those whose range leaves fp32's,
 // take code_of, which compares D with the midpoint.
 //
-// Minimum and maximum of a group are taken on bf16 pairs in an integer order
-// (two values an instruction), and cross the group's threads in one word.
+// Minimum and maximum of a group are taken on bf16 pairs (two values an
+// instruction; a NaN stays) and cross the group's threads in one word.
 //
 // A thread holds eight channels (16 bytes of bf16, one word of codes) of K and
 // of V of two tokens, so that four loads are in flight.  Bound: issue slots
@@ -50,9 +50,16 @@ __device__ __forceinline__ uint32_t code_of(float x, float m, float s, float inv
   return static_cast<uint32_t>(static_cast<int>(f)) + (up ? 1u : 0u);
 }
 
-// Two bf16 values as 16-bit integers of the same order, and back (its inverse).
-__device__ __forceinline__ uint32_t ordered(uint32_t w) {
-  return w ^ (((w >> 15) & 0x00010001u) * 0x7fffu);
+// Larger and smaller of bf16 pairs; NaN if either is.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Quantises this thread's eight channels; kLanes threads share a group.
@@ -60,26 +67,22 @@ __device__ __forceinline__ uint32_t ordered(uint32_t w) {
 template <int kLanes>
 __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t* param) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  // Largest value, largest of the negated order (the smallest value), and the
-  // smallest size above zero (sizes moved by 0x7fff: zero is then the top of
-  // the signed range, and no half carries into the other).
-  uint32_t top = ordered(w[0]), bot = ~top, least = 0x7fff7fffu;
-#pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    const uint32_t o = ordered(w[i]);
-    top = __vmaxs2(top, o);
-    bot = __vmaxs2(bot, ~o);
-  }
+  // Largest and smallest value, and the smallest size above zero (sizes moved by
+  // 0x7fff: zero is then the top of the signed range, and no half carries into
+  // the other).
+  const uint32_t top = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+  const uint32_t bot = min_bf16x2(min_bf16x2(w[0], w[1]), min_bf16x2(w[2], w[3]));
+  uint32_t least = 0x7fff7fffu;
 #pragma unroll
   for (int i = 0; i < 4; ++i) least = __vmins2(least, (w[i] & 0x7fff7fffu) + 0x7fff7fffu);
-  // (largest, largest negated) of the halves, then of the group's threads
-  uint32_t both = __vmaxs2(__byte_perm(top, bot, 0x5410), __byte_perm(top, bot, 0x7632));
+  // (largest, smallest negated) of the halves, then of the group's threads
+  uint32_t both = max_bf16x2(__byte_perm(top, bot, 0x5410) ^ 0x80000000u,
+                             __byte_perm(top, bot, 0x7632) ^ 0x80000000u);
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) both = __vmaxs2(both, __shfl_xor_sync(0xffffffffu, both, d));
-  const uint32_t range = ordered(both ^ 0xffff0000u);  // low: largest, high: smallest, bf16
-  const float hi = bf16_lo(range), lo = bf16_hi(range);
+  for (int d = 1; d < kLanes; d <<= 1) both = max_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, d));
+  const float hi = bf16_lo(both), lo = -bf16_hi(both);
   const float big = fmaxf(fabsf(lo), fabsf(hi));
-  // An infinity, or a NaN: one of either sign is the largest or the smallest.
+  // An infinity, or a NaN.
   if (!(big < INFINITY)) {
     *param = 0x7fc07fc0u;
     return 0;
@@ -90,8 +93,11 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t* param) {
   if (lo != 0.f) small = fminf(small, fabsf(lo));
   const bool near = big < 0x1p125f && span > 0x1p-60f && !(small < 0x1p-13f * big);
   if (near) {
-    const float s = round_bf16(__fdiv_rn(span, 15.f));
-    *param = (__float_as_uint(s) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+    // span / 15 as the quotients below: an approximate one and its exact remainder
+    constexpr float k15th = 1.f / 15.f;
+    const float q15 = span * k15th;
+    *param = pack_bf16(fmaf(fmaf(-15.f, q15, span), k15th, q15), lo);
+    const float s = bf16_lo(*param);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     const uint64_t m2 = f2_pack(lo, lo), s2 = f2_pack(-s, -s), i2 = f2_pack(inv, inv);
@@ -143,10 +149,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t* param) {
 }
 
 // grid (token blocks, heads); a block holds kTokens * kRowThreads / (d / 8) tokens.
-template <int kGroup>
+template <int kD, int kGroup>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsArgs a) {
-  const int tpr = a.d / 8;  // threads a row: 8, 16 or 32, so a warp holds whole rows
-  const int pass = kRowThreads / tpr;
+  constexpr int tpr = kD / 8;  // threads a row: 8, 16 or 32, so a warp holds whole rows
+  constexpr int pass = kRowThreads / tpr;
   const int t0 = blockIdx.x * (kTokens * pass) + threadIdx.x / tpr;
   const int part = threadIdx.x % tpr;
   const int h = blockIdx.y;
@@ -187,20 +193,26 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4RowsAr
   }
 }
 
+// The eight values of a word of codes: 0x4300 | c is 128 + c in bf16, c follows
+// exactly, and one bf16 FMA rounds minimum + scale * c once.
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t param) {
-  const float s = bf16_lo(param), m = bf16_hi(param);
+  const uint32_t s = __byte_perm(param, param, 0x1010), m = __byte_perm(param, param, 0x3232);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)  // s * code has at most 12 significant bits: one rounding in the fma
-    w[i] = pack_bf16(fmaf(static_cast<float>((codes >> (4 * i)) & 15u), s, m),
-                     fmaf(static_cast<float>((codes >> (4 * i + 16)) & 15u), s, m));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((codes >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("{\n\t.reg .b32 t;\n\t"
+        "add.rn.bf16x2 t, %1, %2;\n\t"
+        "fma.rn.bf16x2 %0, t, %3, %4;\n\t}"
+        : "=r"(w[i])
+        : "r"(c), "r"(0xc300c300u), "r"(s), "r"(m));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kGroup>
+template <int kD, int kGroup>
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4RowsArgs a) {
-  const int tpr = a.d / 8;
-  const int pass = kRowThreads / tpr;
+  constexpr int tpr = kD / 8, pass = kRowThreads / tpr;
   const int t0 = blockIdx.x * (kTokens * pass) + threadIdx.x / tpr;
   const int part = threadIdx.x % tpr;
   const int h = blockIdx.y;
@@ -243,18 +255,44 @@ dim3 rows_grid(const Kv4RowsArgs& a) {
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t stream) {
-  if (a.group == 32)
-    kv4_append_kernel<32><<<rows_grid(a), kRowThreads, 0, stream>>>(a);
-  else
-    kv4_append_kernel<64><<<rows_grid(a), kRowThreads, 0, stream>>>(a);
+  const dim3 grid = rows_grid(a);
+  const bool g32 = a.group == 32;
+  switch (a.d) {
+    case 64:
+      if (g32) kv4_append_kernel<64, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_append_kernel<64, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    case 128:
+      if (g32) kv4_append_kernel<128, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_append_kernel<128, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    case 256:
+      if (g32) kv4_append_kernel<256, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_append_kernel<256, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    default: return cudaErrorInvalidValue;
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_gather(const Kv4RowsArgs& a, cudaStream_t stream) {
-  if (a.group == 32)
-    kv4_gather_kernel<32><<<rows_grid(a), kRowThreads, 0, stream>>>(a);
-  else
-    kv4_gather_kernel<64><<<rows_grid(a), kRowThreads, 0, stream>>>(a);
+  const dim3 grid = rows_grid(a);
+  const bool g32 = a.group == 32;
+  switch (a.d) {
+    case 64:
+      if (g32) kv4_gather_kernel<64, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_gather_kernel<64, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    case 128:
+      if (g32) kv4_gather_kernel<128, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_gather_kernel<128, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    case 256:
+      if (g32) kv4_gather_kernel<256, 32><<<grid, kRowThreads, 0, stream>>>(a);
+      else kv4_gather_kernel<256, 64><<<grid, kRowThreads, 0, stream>>>(a);
+      break;
+    default: return cudaErrorInvalidValue;
+  }
   return cudaGetLastError();
 }
 
