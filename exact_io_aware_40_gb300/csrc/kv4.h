@@ -90,7 +90,7 @@ struct Kv4AttnArgs {
 
 // CTAs of a launch never exceed these, so that the workspace's size does not
 // depend on the device.
-constexpr int kKv4MaxCtas = 960;       // few query rows (kv4_attn.cu)
+constexpr int kKv4MaxCtas = 640;       // few query rows (kv4_attn.cu)
 constexpr int kKv4MaxChunkCtas = 160;  // many (kv4_chunk.cu)
 // Query rows of one CTA's block, given the most rows (queries x heads per K/V
 // head) a request may have; 128 and more select the kernel for many.

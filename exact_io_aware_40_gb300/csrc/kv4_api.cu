@@ -159,7 +159,7 @@ fa_status fa_kv4_attn(const void* Q, const void* cache, const int32_t* block_tab
   if (!Q || !cache || !block_table || !cu_q || !kv_len || !O || !L || !workspace)
     return FA_ERR_INVALID_ARG;
   if (B < 1 || total_q < 1 || max_q < 1 || Hq < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f) || window < -1) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * kLog2e) || !(scale > 0.f) || window < -1) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(num_pages, page_size, d, group, Hkv);
   if (st != FA_OK) return st;
   if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;

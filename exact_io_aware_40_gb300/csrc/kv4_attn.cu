@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, q = lane & 3;  // row / column pair of the product's fragments
 
-  const Kv4Share share = kv4_share<kTile, kAttnThreads>(a, C::kRows, a.whole_items ? 1 : kLead + 1, scratch);
+  const Kv4Share share = kv4_share<kTile, kAttnThreads, false>(a, C::kRows, a.whole_items ? 1 : kLead + 1, scratch);
   long long u = share.per * blockIdx.x;
   const long long u_end = min(share.total, u + share.per);
   if (tid == 0 && u >= share.total) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);

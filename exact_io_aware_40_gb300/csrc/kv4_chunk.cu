@@ -191,7 +191,7 @@ template <int kBlockRows>
 struct Tiles {
   Kv4Walk<kTile> w;
   long long u, u_next, u_end;
-  int t, first, last;  // tile of the item; the part of it in this share
+  int first, last;  // the item's tiles in this share
 
   __device__ __forceinline__ void begin(const Kv4AttnArgs& a, const Kv4Share& s) {
     u = s.per * blockIdx.x;
@@ -201,7 +201,6 @@ struct Tiles {
   }
   __device__ __forceinline__ void open(const Kv4AttnArgs& a) {
     u_next = kv4_part(a, w, u, u_end, &first, &last);
-    t = first;
   }
   // To the next item with tiles in this share; false if there is none.
   __device__ __forceinline__ bool next_item(const Kv4AttnArgs& a) {
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const Kv4Share share = kv4_share<kTile, kThreads>(a, C::kBlockRows, kLead + 2, scratch);
+  const Kv4Share share = kv4_share<kTile, kThreads, true>(a, C::kBlockRows, kLead + 2, scratch);
   if (share.per * blockIdx.x >= share.total) {
     if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;

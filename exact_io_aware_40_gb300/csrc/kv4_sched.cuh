@@ -76,13 +76,34 @@ __device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnArgs& a, const Kv4Req
   return k;
 }
 
-template <int kTile>
+// A request of more blocks of rows than this is looked through by a whole warp
+// (65536 queries with a window: 145 -> 54 us).  The kernel for few rows has no
+// such requests (kMany false), and the choice would cost it half a microsecond.
+constexpr int kKv4OwnBlocks = 4;
+
+// Places of request b (none: -1) in the list.  Every lane of a warp calls it, each
+// with a request of its own.
+template <int kTile, bool kMany>
 __device__ __forceinline__ long long kv4_units(const Kv4AttnArgs& a, int b, int block_rows,
                                                bool* bad) {
-  const Kv4Req r = kv4_request(a, b, bad);
+  Kv4Req r{0, 0, 0};
+  if (b >= 0) r = kv4_request(a, b, bad);
   const int blocks = (r.n * a.per_kv + block_rows - 1) / block_rows;
   long long n = 0;
-  for (int rb = 0; rb < blocks; ++rb) n += kv4_block<kTile>(a, r, rb, block_rows).units;
+  if (!kMany || blocks <= kKv4OwnBlocks)
+    for (int rb = 0; rb < blocks; ++rb) n += kv4_block<kTile>(a, r, rb, block_rows).units;
+  if (!kMany) return n * a.Hkv;
+  uint32_t many = __ballot_sync(0xffffffffu, blocks > kKv4OwnBlocks);
+  for (; many; many &= many - 1) {
+    const int lane = threadIdx.x & 31, whose = __ffs(many) - 1;
+    const Kv4Req o{0, __shfl_sync(0xffffffffu, r.n, whose), __shfl_sync(0xffffffffu, r.kv, whose)};
+    const int o_blocks = __shfl_sync(0xffffffffu, blocks, whose);
+    long long sum = 0;
+    for (int rb = lane; rb < o_blocks; rb += 32) sum += kv4_block<kTile>(a, o, rb, block_rows).units;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == whose) n = sum;
+  }
   return n * a.Hkv;
 }
 
@@ -95,28 +116,57 @@ __device__ __forceinline__ long long kv4_div(long long n, long long d) {
 
 struct Kv4Share {
   long long total, per;  // places in the list, and in a share
-  long long begin;       // first place that belongs to request b
-  int b;
+  long long begin;       // first place that belongs to blocks of rows from rb on of request b
+  int b, rb;             // (of few blocks: rb is 0 and the walk looks for its own)
 };
+
+// Finds the block of rows of request s.b that holds place u0, if there are many.
+// Every lane of a warp calls it.
+template <int kTile>
+__device__ __forceinline__ void kv4_find_block(const Kv4AttnArgs& a, int block_rows, long long u0, Kv4Share* s) {
+  bool bad = false;
+  const int lane = threadIdx.x & 31;
+  const Kv4Req r = kv4_request(a, s->b, &bad);
+  const int blocks = (r.n * a.per_kv + block_rows - 1) / block_rows;
+  if (blocks <= kKv4OwnBlocks) return;
+  for (int base = 0; base < blocks; base += 32) {
+    const int rb = base + lane;
+    const long long mine =
+        rb < blocks ? static_cast<long long>(kv4_block<kTile>(a, r, rb, block_rows).units) * a.Hkv : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, u0 < s->begin + incl);
+    if (who) {
+      s->rb = base + __ffs(who) - 1;
+      s->begin += __shfl_sync(0xffffffffu, incl - mine, __ffs(who) - 1);
+      return;
+    }
+    s->begin += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
 
 // Every thread of the block finds the block's share; `scratch` holds
 // kThreads / 32 + 2 long longs.  Shares are at least min_tiles long.  begin/b are
 // set when the share is not empty (blockIdx.x * per < total).  Up to 128 requests
 // every warp adds up all of them by itself, which spares the barriers.
-template <int kTile, int kThreads>
+template <int kTile, int kThreads, bool kMany>
 __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_rows, int min_tiles,
                                               long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   Kv4Share s;
-  s.b = 0;
+  s.b = s.rb = 0;
   s.begin = 0;
   if (a.B <= 128) {
     long long mine[4], at[4];  // request 32 i + lane: its tiles, those before it
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int b = 32 * i + lane;
-      mine[i] = b < a.B ? kv4_units<kTile>(a, b, block_rows, &bad) : 0;
+      if (32 * i < a.B) mine[i] = kv4_units<kTile, kMany>(a, b < a.B ? b : -1, block_rows, &bad);
     }
     if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
     s.total = 0;
@@ -144,11 +194,13 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
         s.begin = __shfl_sync(0xffffffffu, at[i], __ffs(who) - 1);
       }
     }
+    if (kMany) kv4_find_block<kTile>(a, block_rows, u0, &s);
     return s;
   }
-  long long first = tid < a.B ? kv4_units<kTile>(a, tid, block_rows, &bad) : 0;
+  const long long first = kv4_units<kTile, kMany>(a, tid < a.B ? tid : -1, block_rows, &bad);
   long long sum = first;
-  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += kv4_units<kTile>(a, b, block_rows, &bad);
+  for (int base = kThreads; base < a.B; base += kThreads)
+    sum += kv4_units<kTile, kMany>(a, base + tid < a.B ? base + tid : -1, block_rows, &bad);
   if (bad && blockIdx.x == 0) atomicCAS(a.input_err, 0, 1);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -164,7 +216,7 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
   for (int base = 0; base < a.B; base += kThreads) {
     const int b = base + tid;
     long long v = first;
-    if (base) v = b < a.B ? kv4_units<kTile>(a, b, block_rows, &bad) : 0;
+    if (base) v = kv4_units<kTile, kMany>(a, b < a.B ? b : -1, block_rows, &bad);
     long long incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -186,6 +238,7 @@ __device__ __forceinline__ Kv4Share kv4_share(const Kv4AttnArgs& a, int block_ro
   __syncthreads();
   s.begin = scratch[kThreads / 32];
   s.b = static_cast<int>(scratch[kThreads / 32 + 1]);
+  if (kMany) kv4_find_block<kTile>(a, block_rows, u0, &s);
   return s;
 }
 
@@ -211,6 +264,10 @@ struct Kv4Walk {
     b = s.b;
     item = s.begin;
     open(a, block_rows);
+    if (s.rb > 0) {
+      rb = s.rb;
+      blk = kv4_block<kTile>(a, req, rb, block_rows);
+    }
     while (u >= item + static_cast<long long>(blk.units) * a.Hkv) {
       item += static_cast<long long>(blk.units) * a.Hkv;
       ++rb;

@@ -60,7 +60,7 @@ def test_gather_refuses(lib, bad, status):
     (dict(Q=NULL), 1), (dict(Q=ODD), 1), (dict(ws=NULL), 1), (dict(ws=ctypes.c_void_p(0x10010)), 1),
     (dict(bytes=64), 1), (dict(B=0), 1), (dict(total=0), 1), (dict(max_q=0), 1), (dict(Hq=7), 1),
     (dict(Hq=0), 1), (dict(d=80), 2), (dict(qt=12), 1), (dict(qh=-8), 1), (dict(window=-2), 1),
-    (dict(scale=ctypes.c_float(0.0)), 1), (dict(scale=ctypes.c_float(float("nan"))), 1), (dict(width=0), 1),
+    (dict(scale=ctypes.c_float(0.0)), 1), (dict(scale=ctypes.c_float(3e38)), 1), (dict(scale=ctypes.c_float(float("nan"))), 1), (dict(width=0), 1),
     (dict(width=1 << 27), 2), (dict(max_q=1 << 29), 2), (dict(page=48), 2), (dict(total=(1 << 30) + 1), 2)])
 def test_attention_refuses(lib, bad, status):
     assert call(lib.fa_kv4_attn, ATTN, **bad) == status

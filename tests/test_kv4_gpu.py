@@ -474,6 +474,18 @@ def test_attention_of_many_requests(fa, B, nq):
     check(fa, attention_case(B + 1, lens, n, 1, 8, 128, 64, 64))
 
 
+@pytest.mark.parametrize("d,per,window", [(64, 4, -1), (64, 4, 50), (128, 4, 7), (256, 2, 200)])
+@pytest.mark.parametrize("others", [1, 140])
+def test_attention_of_many_blocks_of_rows(fa, d, per, window, others):
+    # a request of more blocks than a warp has lanes, beside short ones before and behind it
+    lens = [40 + 3 * b for b in range(others)]
+    n = [b % 5 for b in range(others)]
+    at = others // 2
+    c = attention_case(d + others, lens[:at] + [2411] + lens[at:], n[:at] + [2203] + n[at:], 1, per, d, 32, 16)
+    c["window"] = window
+    check(fa, c)
+
+
 @pytest.mark.parametrize("nq", [1, 12, 100])
 def test_attention_is_bitwise_repeatable(fa, nq):
     import torch
