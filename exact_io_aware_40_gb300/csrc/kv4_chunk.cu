@@ -535,6 +535,11 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128u * g;  // S
     const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kColO + HD * g;
     uint8_t* sq = smem + C::kOffQ + g * C::kQTile;
+    const uint32_t sq_u32 = sb + C::kOffQ + g * C::kQTile;
+    constexpr int kChunks = HD / 8;  // 16 bytes each of a row of bf16 or fp16
+    auto row_chunk = [](int r, int c) {  // where chunk c of row r is (128-byte swizzle)
+      return (c >> 3) * C::kQAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
     uint8_t* sqx = smem + C::kOffQEx + g * C::kQEx;
     int4 record = make_int4(0, 0, 0, 0);
     bool ok = true, first_item = true;
@@ -563,40 +568,59 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
 
       // Q: the row scaled by a power of two into [2^7, 2^8), in fp16, and the
       // slots of its sums over the groups.  The products of the item before
-      // have all completed (its O was read), so the tile is free.
+      // have all completed (its O was read), so the tile is free.  The warp copies
+      // its rows whole rows at a time (a thread's own row would be a line for each
+      // lane), then each thread works on its own.
       float row_scale;
       {
-        const uint16_t* src = a.Q + static_cast<long long>(k.req.start + t) * a.q_ts +
-                              static_cast<long long>(head) * a.q_hs;
-        uint32_t top = 0;
+        const long long q_at = have ? static_cast<long long>(k.req.start + t) * a.q_ts +
+                                          static_cast<long long>(head) * a.q_hs
+                                    : -1;
 #pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint4 x = have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+          const long long at = __shfl_sync(0xffffffffu, q_at, r);
+          cp_async16(sq_u32 + row_chunk((warp & 3) * 32 + r, c), a.Q + max(at, 0ll) + 8 * c, at >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int c = 0; c < kChunks; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sq + row_chunk(row, c));
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                                        __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
         }
+        // (A row below 2^-119 is left below 2^7: fp16's step, 2^-24, still is
+        // 2^-17 of the smallest bf16.)
         const int et = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7) - 127;  // -127: zero
-        // The power of two is applied in two halves: either alone is in range.
-        const int up = 7 - max(et, -126);
-        const float u0 = pow2i(up / 2), u1 = pow2i(up - up / 2);
-        row_scale = a.scale_log2 * pow2i(-(up / 2)) * pow2i(-(up - up / 2));
-        float sum = 0.f;
+        const int up = min(7 - et, 126);
+        const float unit = pow2i(up);
+        row_scale = a.scale_log2 * pow2i(-up);
+        const uint64_t unit2 = f2_pack(unit, unit);
+        uint64_t sum2 = 0;
 #pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint4 x = have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < kChunks; ++c) {
+          uint4* place = reinterpret_cast<uint4*>(sq + row_chunk(row, c));
+          const uint4 x = *place;
           const uint32_t in[4] = {x.x, x.y, x.z, x.w};
           uint32_t out[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float lo = __uint_as_float(in[i] << 16) * u0 * u1;
-            const float hi = __uint_as_float(in[i] & 0xffff0000u) * u0 * u1;
-            sum += lo + hi;
+            const uint64_t y =
+                f2_mul(f2_pack(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), unit2);
+            sum2 = f2_add(sum2, y);
+            float lo, hi;
+            f2_unpack(y, lo, hi);
             out[i] = pack_f16(lo, hi);
           }
-          *reinterpret_cast<uint4*>(sq + (c / 8) * C::kQAtom + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+          *place = make_uint4(out[0], out[1], out[2], out[3]);
           if ((c + 1) % (GROUP / 8) == 0) {
             const int grp = c / (GROUP / 8);
+            float s0, s1;
+            f2_unpack(sum2, s0, s1);
+            const float sum = s0 + s1;
             const __half h = __float2half_rn(sum), l = __float2half_rn(sum - __half2float(h));
             const __half slot[3] = {h, h, l};
 #pragma unroll
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
               *reinterpret_cast<__half*>(sqx + (row >> 3) * C::kExRow8 + (kk >> 3) * 128 +
                                          (row & 7) * 16 + (kk & 7) * 2) = slot[e];
             }
-            sum = 0.f;
+            sum2 = 0;
           }
         }
       }
@@ -725,26 +749,45 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       const long long o_row = static_cast<long long>(k.req.start + t) * a.Hq + head;
       const long long p_row =
           (2ll * blockIdx.x + (first_item && first_tile > 0 ? 0 : 1)) * C::kBlockRows + kRows * g + row;
+      // Out by way of the item's Q tile, which has served: a thread puts its row
+      // there, as bf16 or one half after the other as fp32, and the warp writes
+      // whole rows.
+      const long long out_at = !have ? -1 : whole ? o_row * (HD * 2) : p_row * (HD * 4);  // bytes
 #pragma unroll 1
-      for (int c = 0; c < HD / 16; ++c) {
-        uint32_t o[16];
-        tmem_ld16(to + 16 * c, o);
-        tmem_wait_ld();
-        const bool odd = (nan_groups >> (16 * c / GROUP)) & 1;
-        float x[16];
+      for (int part = 0; part < (whole ? 1 : 2); ++part) {
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < (whole ? HD / 16 : HD / 32); ++c) {
+          const int col = 16 * c + part * (HD / 2);
+          uint32_t o[16];
+          tmem_ld16(to + col, o);
+          tmem_wait_ld();
+          const bool odd = (nan_groups >> (col / GROUP)) & 1;
+          float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = odd ? __int_as_float(0x7fffffff) : __uint_as_float(o[e]) * f;
-        if (!have) continue;
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.O + o_row * HD + 16 * c);
+          for (int e = 0; e < 16; ++e) x[e] = odd ? __int_as_float(0x7fffffff) : __uint_as_float(o[e]) * f;
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            dst[e] = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
-                                pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + p_row * HD + 16 * c);
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(sq + row_chunk(row, 2 * c + e)) =
+                  make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
+                             pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<float4*>(sq + row_chunk(row, 4 * c + e)) =
+                  make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          }
+        }
+        __syncwarp();
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.O)
+                             : reinterpret_cast<uint8_t*>(a.part_o) + part * (HD * 2);
+#pragma unroll 4
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+          const long long at = __shfl_sync(0xffffffffu, out_at, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(sq + row_chunk((warp & 3) * 32 + r, c));
+          if (at >= 0) *reinterpret_cast<uint4*>(dst + at + 16 * c) = x;
         }
       }
       if (have) {
@@ -756,6 +799,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       // O has been read before the next item's products may overwrite it: they
       // wait for p_full, which this warp signals after this point.
       tc_fence_before();
+      __syncwarp();  // and the tile before the next item's Q
       first_item = false;
     } while (next_item());
     if (tid == 0) a.split[blockIdx.x] = record;
