@@ -1,7 +1,7 @@
 // kv4_attn.cu -- attention over the paged 4-bit cache for few query rows.
 //
-// Up to 32 rows (queries x query heads of one K/V head) share each read of the
-// cache; one read of the keys and values is all the memory traffic there is, so
+// Blocks of 8, 16 or 32 rows (queries x query heads of one K/V head) share each
+// read of the cache; one read of the keys and values is all the memory traffic there is, so
 // the kernel is built around it: a warp walks the cache on its own, 32 tokens at
 // a time, with its copies (cp.async) several steps ahead and no barrier with any
 // other warp until its item ends.  Per 16 tokens and a K/V head:
@@ -33,6 +33,7 @@
 // at most (V).
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -836,7 +837,7 @@ cudaError_t launch_attn_rows(const Kv4AttnArgs& a, cudaStream_t stream) {
   if (block >= 128) {
     int ctas = 0;
     const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
-    return e != cudaSuccess ? e : launch_merge<HD>(a, ctas, block, stream);
+    return e != cudaSuccess || a.whole_items ? e : launch_merge<HD>(a, ctas, block, stream);
   }
   if (block == 8) return launch_attn<HD, GROUP, 1>(a, stream);
   if constexpr (HD <= 128)
@@ -851,16 +852,20 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 // The block of rows that serves `rows` best.  More rows in a block cost a warp
-// registers (32 at d = 128 and 16 at d = 256 spill) and products, further blocks
-// read the cache again; the kernel for many rows converts every tile once.
-// Measured, 16 requests of 8192 tokens, in us for blocks of 8, 16, 32, many:
-//   d = 64   16 rows  95  70 102 305    64 rows 347 236 198 309   128: 680 458 381 314
-//   d = 128  16 rows  83  66 157 185    48 rows 225 163 287 189    64: 293 211 291 190
-//   d = 256  16 rows  77  84   - 163    32 rows 137 140   - 166    48: 202 189   - 167
+// registers (32 at d = 128 and 16 at d = 256 spill, also with the queries in
+// shared memory) and products, further blocks read the cache again; the kernel
+// for many rows converts every tile once.
+// Measured in us for blocks of 8, 16, 32, many, with 16 requests of 8192 tokens
+// and with 64 of 768 (8 K/V heads at d = 128):
+//   d = 64   32 rows 169 123 108 224 |  94  73  71 142     d = 128   16 rows  77  73 154 |  43  40 103
+//            48      246 174 193 225 | 136 102 125 142               24      112 120 156 |  62  67 105
+//            64      324 228 194 226 | 177 127 127 143               48      208 170 157 | 110  97 107
+//            80      399 279 278 226 | 217 165 179 145               56      240 217 158 | 120 124 108
+//   d = 256  32 rows 136 (8), 164 (many) | 78, 91              40 rows 168, 164 | 95, 91
 int kv4_attn_rows(int d, int rows) {
   if (rows <= 8) return 8;
-  if (d == 64) return rows <= 16 ? 16 : rows <= 96 ? 32 : 256;
-  if (d == 128) return rows <= 48 ? 16 : 256;
+  if (d == 64) return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 16 : rows <= 64 ? 32 : 256;
+  if (d == 128) return rows <= 16 ? 16 : rows <= 24 ? 8 : rows <= 48 ? 16 : 256;
   return rows <= 32 ? 8 : 128;
 }
 
@@ -885,10 +890,15 @@ cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cu
   a.part_stat = reinterpret_cast<float2*>(ws);
   ws += align256(parts * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(ws);
-  // With at most four tiles to an item, cutting it saves less than the merge
-  // costs (one more launch).
-  a.whole_items = kv4_attn_rows(d, a.max_q * a.per_kv) < 128 &&
-                  (static_cast<long long>(a.max_pages) << a.lay.page_shift) <= 4 * kTile;
+  // Cutting items of few keys saves less than it costs (the merge, and a second
+  // change of items): 512 tokens here, and for many rows 1024, if there are not
+  // many more items than CTAs, over which uneven ones would not even out (8 K/V
+  // heads, d = 128: 512 queries 34 -> 25 us; but 64 times 512 414 -> 451 us).
+  const int block = kv4_attn_rows(d, a.max_q * a.per_kv);
+  long long span = static_cast<long long>(a.max_pages) << a.lay.page_shift;  // keys of an item, at most
+  if (a.window >= 0) span = std::min(span, static_cast<long long>(a.window) + block / a.per_kv + 2);
+  const long long items = (static_cast<long long>(a.total_q) * a.per_kv / block + a.B) * a.Hkv;
+  a.whole_items = block < 128 ? span <= 512 : span <= 1024 && items <= 2 * sm_count();
   const bool g32 = group == 32;
   switch (d) {
     case 64: return g32 ? launch_attn_rows<64, 32>(a, stream) : launch_attn_rows<64, 64>(a, stream);

@@ -12,7 +12,7 @@
 // so an item's tiles are led in the list by `lead` places that stand for that.  An item that a share's end
 // cuts is finished from partial results by a second kernel.  Where no item is
 // long (whole_items) a place in the list is an item instead, and that kernel is
-// not needed.
+// not launched.
 #pragma once
 #include "kv4.h"
 
