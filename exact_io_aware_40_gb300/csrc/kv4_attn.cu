@@ -31,6 +31,12 @@
 // agree; token_of and the swizzle of the staged 16-byte chunks (twist) are chosen
 // so that a warp's reads of its staged codes meet no bank twice (K), or twice
 // at most (V).
+//
+// Measured (d = 128, 16 requests of 8192 tokens, 8 K/V heads, 8 query heads each):
+// 46 us for 168 MB of cache, of which 10 to 15 us are paid once a call (launch,
+// shares, first copies, the exchange between warps, merge); in between 5.2 to 5.6
+// TB/s.  Bound: issue slots (57 % taken, with 16 warps an SM and each warp's chain
+// from codes to weights to hide), about 380 instructions for 16 tokens of a head.
 #include <cuda_fp16.h>
 
 #include <algorithm>

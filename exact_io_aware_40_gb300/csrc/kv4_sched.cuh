@@ -268,7 +268,7 @@ struct Kv4Walk {
       rb = s.rb;
       blk = kv4_block<kTile>(a, req, rb, block_rows);
     }
-    while (u >= item + static_cast<long long>(blk.units) * a.Hkv) {
+    while (rb + 1 < blocks && u >= item + static_cast<long long>(blk.units) * a.Hkv) {
       item += static_cast<long long>(blk.units) * a.Hkv;
       ++rb;
       blk = kv4_block<kTile>(a, req, rb, block_rows);

@@ -486,6 +486,17 @@ def test_attention_of_many_blocks_of_rows(fa, d, per, window, others):
     check(fa, c)
 
 
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)])
+@pytest.mark.parametrize("window", [-1, 1200])
+def test_attention_of_chunks_that_shares_cut(fa, d, group, window):
+    # longer than what is left whole: parts of items, some shares with two items, and the merge
+    c = attention_case(d + group, [1901, 40, 2603, 1300], [301, 5, 77, 1], 2, 4, d, group, 64)
+    c["window"] = window
+    check(fa, c)
+    c["causal"] = window >= 0
+    check(fa, c)
+
+
 @pytest.mark.parametrize("nq", [1, 12, 100])
 def test_attention_is_bitwise_repeatable(fa, nq):
     import torch
@@ -727,4 +738,20 @@ def test_two_streams_with_workspaces_of_their_own(fa):
     torch.cuda.synchronize()
     for (o, l), (o1, l1) in zip(alone, got):
         assert torch.equal(o, o1) and torch.equal(l, l1)
+    fa.fa_check_error()
+
+
+def test_two_streams_of_chunks(fa):
+    import torch
+    cases = [attention_case(111 + i, [1500, 300], [130, 90], 1, 4, d, 32, 64) for i, d in enumerate([64, 128])]
+    alone = [run_attention(fa, c) for c in cases]
+    args = [(dev_bf16(R.bf16_bits(c["q"])), dev(c["cache"]), dev(c["table"]), dev(c["cu"]), dev(c["kv_len"]))
+            for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [fa.kv4_attention(*a, 130, 64, 32, stream=s.cuda_stream) for a, s in zip(args, streams)]
+        torch.cuda.synchronize()
+        for (o, l), (o1, l1) in zip(alone, got):
+            assert torch.equal(o, o1) and torch.equal(l, l1)
     fa.fa_check_error()
