@@ -96,6 +96,9 @@ constexpr int kKv4MaxChunkCtas = 160;  // many (kv4_chunk.cu)
 // head) a request may have; 128 and more select the kernel for many.
 int kv4_attn_rows(int d, int rows);
 size_t kv4_attn_workspace(int d, int rows);
+// Are a call's items left whole, so that nothing is merged?  `table` is the tokens
+// a row of the block table can hold.
+bool kv4_attn_whole(int d, int max_q, int per_kv, int Hkv, int B, int total_q, long long table, int window);
 cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cudaStream_t stream);
 // The kernel for many rows; *ctas: CTAs launched, for the merge that follows.
 cudaError_t launch_kv4_chunk(int d, int group, const Kv4AttnArgs& a, cudaStream_t stream, int* ctas);

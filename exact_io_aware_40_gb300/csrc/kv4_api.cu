@@ -150,14 +150,26 @@ size_t fa_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
   return fa::kv4_attn_workspace(d, rows > (1 << 30) ? (1 << 30) : static_cast<int>(rows));
 }
 
+size_t fa_kv4_attn_call_workspace_bytes(int B, int total_q, int max_q, int Hq, int Hkv, int d,
+                                        int max_pages, int page_size, int window) {
+  const size_t most = fa_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q);
+  if (most == 0 || B < 1 || total_q < 1 || max_pages < 1 || !page_ok(page_size) || window < -1 ||
+      static_cast<long long>(max_q) * (Hq / Hkv) > 0x3fffffffLL)
+    return most;  // (the call says what is wrong)
+  return fa::kv4_attn_whole(d, max_q, Hq / Hkv, Hkv, B, total_q,
+                            static_cast<long long>(max_pages) * page_size, window)
+             ? 0
+             : most;
+}
+
 fa_status fa_kv4_attn(const void* Q, const void* cache, const int32_t* block_table,
                       const int32_t* cu_q, const int32_t* kv_len, void* O, float* L, int B,
                       int total_q, int max_q, int Hq, int Hkv, int d, int q_token_stride,
                       int q_head_stride, int num_pages, int max_pages, int page_size, int group,
                       float scale, int causal, int window, void* workspace,
                       size_t workspace_bytes, fa_stream_t stream) {
-  if (!Q || !cache || !block_table || !cu_q || !kv_len || !O || !L || !workspace)
-    return FA_ERR_INVALID_ARG;
+  if (!Q || !cache || !block_table || !cu_q || !kv_len || !O || !L) return FA_ERR_INVALID_ARG;
+  if (!workspace && workspace_bytes) return FA_ERR_INVALID_ARG;
   if (B < 1 || total_q < 1 || max_q < 1 || Hq < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale * kLog2e) || !(scale > 0.f) || window < -1) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(num_pages, page_size, d, group, Hkv);
@@ -170,7 +182,10 @@ fa_status fa_kv4_attn(const void* Q, const void* cache, const int32_t* block_tab
   if (!strides_ok(q_token_stride, q_head_stride) || !aligned(Q, 16) || !aligned(O, 16) ||
       !aligned(cache, 16) || !aligned(L, 4) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
       !aligned(kv_len, 4) || !aligned(workspace, 256) ||
-      workspace_bytes < fa_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q))
+      workspace_bytes <
+          (workspace ? fa_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q)
+                     : fa_kv4_attn_call_workspace_bytes(B, total_q, max_q, Hq, Hkv, d, max_pages,
+                                                        page_size, window)))
     return FA_ERR_INVALID_ARG;
   fa::ErrorWords err;
   const int es = fa::error_words(&err);

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
   const Kv4Share share = kv4_share<kTile, kAttnThreads, false>(a, C::kRows, a.whole_items ? 1 : kLead + 1, scratch);
   long long u = share.per * blockIdx.x;
   const long long u_end = min(share.total, u + share.per);
-  if (tid == 0 && u >= share.total) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0 && u >= share.total && !a.whole_items) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (u >= share.total) return;
   bool first_item = true;
   if (tid == 0) {
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
       __syncthreads();
     }
   }
-  if (tid == 0) a.split[blockIdx.x] = record;
+  if (tid == 0 && !a.whole_items) a.split[blockIdx.x] = record;
 }
 
 // Joins the parts of the items that shares' ends cut: one warp per row.  The
@@ -888,6 +888,18 @@ size_t kv4_attn_workspace(int d, int rows) {
          align256(parts * d * sizeof(float));
 }
 
+// Cutting items of few keys saves less than it costs (the merge, and a second
+// change of items): 512 tokens with few rows, and with many 1024, if there are not
+// many more items than CTAs, over which uneven ones would not even out (8 K/V
+// heads, d = 128: 512 queries 34 -> 25 us; but 64 times 512 414 -> 451 us).
+bool kv4_attn_whole(int d, int max_q, int per_kv, int Hkv, int B, int total_q, long long table, int window) {
+  const int block = kv4_attn_rows(d, max_q * per_kv);
+  long long span = table;  // keys of an item, at most
+  if (window >= 0) span = std::min(span, static_cast<long long>(window) + block / per_kv + 2);
+  if (block < 128) return span <= 512;
+  return span <= 1024 && (static_cast<long long>(total_q) * per_kv / block + B) * Hkv <= 2 * sm_count();
+}
+
 cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cudaStream_t stream) {
   const size_t parts = part_rows(d, a.max_q * a.per_kv);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -896,15 +908,8 @@ cudaError_t launch_kv4_attn(int d, int group, Kv4AttnArgs a, void* workspace, cu
   a.part_stat = reinterpret_cast<float2*>(ws);
   ws += align256(parts * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(ws);
-  // Cutting items of few keys saves less than it costs (the merge, and a second
-  // change of items): 512 tokens here, and for many rows 1024, if there are not
-  // many more items than CTAs, over which uneven ones would not even out (8 K/V
-  // heads, d = 128: 512 queries 34 -> 25 us; but 64 times 512 414 -> 451 us).
-  const int block = kv4_attn_rows(d, a.max_q * a.per_kv);
-  long long span = static_cast<long long>(a.max_pages) << a.lay.page_shift;  // keys of an item, at most
-  if (a.window >= 0) span = std::min(span, static_cast<long long>(a.window) + block / a.per_kv + 2);
-  const long long items = (static_cast<long long>(a.total_q) * a.per_kv / block + a.B) * a.Hkv;
-  a.whole_items = block < 128 ? span <= 512 : span <= 1024 && items <= 2 * sm_count();
+  a.whole_items = kv4_attn_whole(d, a.max_q, a.per_kv, a.Hkv, a.B, a.total_q,
+                                 static_cast<long long>(a.max_pages) << a.lay.page_shift, a.window);
   const bool g32 = group == 32;
   switch (d) {
     case 64: return g32 ? launch_attn_rows<64, 32>(a, stream) : launch_attn_rows<64, 64>(a, stream);

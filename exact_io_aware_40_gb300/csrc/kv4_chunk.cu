@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
 
   const Kv4Share share = kv4_share<kTile, kThreads, true>(a, C::kBlockRows, a.whole_items ? 1 : kLead + 2, scratch);
   if (share.per * blockIdx.x >= share.total) {
-    if (tid == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0 && !a.whole_items) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
 
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<HD, GROUP>::kThreads, 1) kv4_chunk_kernel(
       __syncwarp();  // and the tile before the next item's Q
       first_item = false;
     } while (next_item());
-    if (tid == 0) a.split[blockIdx.x] = record;
+    if (tid == 0 && !a.whole_items) a.split[blockIdx.x] = record;
   } else if (warp < kConvV) {
     regs_dec<C::kConvRegs>();
     convert<HD, GROUP, 0>(a, w, smem, sb, bar_kfull, bar_kempty, un, ab);

@@ -68,6 +68,8 @@ def load_library():
     lib.fa_kv4_gather.argtypes = [vp, vp, i, i, i, i, i, i, vp, vp, vp]
     lib.fa_kv4_attn_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_kv4_attn_workspace_bytes.restype = sz
+    lib.fa_kv4_attn_call_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i, i]
+    lib.fa_kv4_attn_call_workspace_bytes.restype = sz
     lib.fa_kv4_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i, i, i, f,
                                 i, i, vp, sz, vp]
     for fn in ("fa_kv4_plan", "fa_kv4_append", "fa_kv4_gather", "fa_kv4_attn",
@@ -553,14 +555,20 @@ def kv4_attention(q, cache, block_table, cu_q, kv_len, max_q, page_size, group=3
     if total == 0 or B == 0:
         return out, lse
     lib = load_library()
+    space = None  # the workspace's address
     if workspace is None:
-        workspace = torch.empty(lib.fa_kv4_attn_workspace_bytes(q_heads, kv_heads, d, max_q),
-                                dtype=torch.uint8, device=at)
+        size = lib.fa_kv4_attn_call_workspace_bytes(B, total, max_q, q_heads, kv_heads, d, max_pages,
+                                                    page_size, window)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=at)
+            space = workspace.data_ptr()
+    else:
+        space, size = workspace.data_ptr(), workspace.numel()
     status = lib.fa_kv4_attn(
         q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
         out.data_ptr(), lse.data_ptr(), B, total, max_q, q_heads, kv_heads, d, q_ts, q_hs, pages,
         max_pages, page_size, group, 1.0 / math.sqrt(d) if scale is None else float(scale),
-        1 if causal else 0, window, workspace.data_ptr(), workspace.numel(),
+        1 if causal else 0, window, space, size,
         torch._C._cuda_getCurrentRawStream(dev))
     if status:
         raise FAError(status, "fa_kv4_attn")

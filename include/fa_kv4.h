@@ -116,7 +116,9 @@ fa_status fa_kv4_gather(const int32_t* slots, const void* cache, int num_pages, 
  *   window          : -1 = none, w >= 0: only keys p - w <= j <= p
  *   workspace       : DEVICE, >= fa_kv4_attn_workspace_bytes() bytes, 256-byte
  *                     aligned; contents on entry are ignored; not to be shared
- *                     by calls that may overlap
+ *                     by calls that may overlap.  Calls for which
+ *                     fa_kv4_attn_call_workspace_bytes() is 0 (short tables or
+ *                     windows) may pass NULL and 0
  * Hq is a multiple of Hkv; query head h reads K/V head h / (Hq / Hkv).
  * d is 64, 128 or 256.  A query that sees no key gets O = 0, L = -inf.  Rows of
  * O and L behind cu_q[B] are left as they were.  Deterministic.  Keys have to be
@@ -125,6 +127,8 @@ fa_status fa_kv4_gather(const int32_t* slots, const void* cache, int num_pages, 
  * any stream capture (it may load device code).
  */
 size_t fa_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q);
+size_t fa_kv4_attn_call_workspace_bytes(int B, int total_q, int max_q, int Hq, int Hkv, int d,
+                                        int max_pages, int page_size, int window);
 fa_status fa_kv4_attn(const void* Q, const void* cache, const int32_t* block_table,
                       const int32_t* cu_q, const int32_t* kv_len, void* O, float* L, int B,
                       int total_q, int max_q, int Hq, int Hkv, int d, int q_token_stride,

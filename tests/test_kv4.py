@@ -81,6 +81,20 @@ def test_sizes(lib):
         assert fa.kv4_attention_workspace_bytes(*bad) == 0
 
 
+def test_workspace_of_a_call(lib):
+    most = lib.fa_kv4_attn_workspace_bytes
+    need = lib.fa_kv4_attn_call_workspace_bytes
+    # B, total_q, max_q, Hq, Hkv, d, max_pages, page_size, window
+    assert need(2, 4, 2, 8, 2, 128, 32, 16, -1) == 0          # 512 tokens
+    assert need(2, 4, 2, 8, 2, 128, 33, 16, -1) == most(8, 2, 128, 2)
+    assert need(2, 4, 2, 8, 2, 128, 1000, 16, 100) == 0       # a window as short
+    assert need(2, 4, 2, 8, 2, 128, 1000, 16, 1000) == most(8, 2, 128, 2)
+    assert need(2, 600, 300, 8, 2, 128, 1000, 16, -1) == most(8, 2, 128, 300)
+    assert need(2, 4, 2, 8, 3, 128, 32, 16, -1) == 0          # no such heads
+    assert call(lib.fa_kv4_attn, ATTN, ws=NULL, bytes=0, width=40) == 1
+    assert call(lib.fa_kv4_attn, ATTN, ws=NULL, bytes=0, width=4, B=0) == 1
+
+
 def test_binding_has_no_cpu_path():
     import torch
     from exact_io_aware_40_gb300 import fa
