@@ -29,14 +29,15 @@
 // fits the tile's largest param.  K's unit multiplies the tile's scores; V's goes
 // into the exponent of P, whose reference then includes the largest unit so far.
 //
-// Measured (d = 128, 2 x 1024 queries of 32 heads over 8K to 16K keys): 490 us, 990
-// TFLOP/s, 0.51 of the measured bf16 peak; a tile takes about 2400 clocks of which
-// the products need 1100.  Bound: the rows' chain from S to P (2270 clocks with the
-// other roles' instructions between its own; about 17 for eight codes, 3.5 for a
-// score, 60 % of the issue slots).  A third stage of K or V is slower (526 to 549
-// us: more in flight at once), and so are weights taken before the maximum is known
-// (545).  At d = 256 one block of 128 rows is all that shared and tensor memory
-// hold, so a converted tile serves half the rows: 475 TFLOP/s.
+// Measured (d = 128, 2 x 1024 queries of 32 heads over 8K to 16K keys): 473 us,
+// 1024 TFLOP/s, 0.52 of the measured bf16 peak; a tile takes about 2300 clocks of
+// which the products need 1100.  Bound: the rows' chain from S to P among the other
+// roles' instructions (2270 of 2880 clocks a tile in a build that counted; about
+// 17 instructions for eight codes, 3.5 for a score, 64 % of the issue slots).  A
+// third stage of K or V is slower (526 to 549 us where two took 515), and so are
+// weights taken before the maximum is known (545 for 515).  At d = 256 one block of
+// 128 rows is all that shared and tensor memory hold, so a converted tile serves
+// half the rows: 560 TFLOP/s.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -174,11 +175,15 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kColO + kBlocks * HD <= kTmemCols, "tensor memory budget");
   // Registers a thread of the warpgroups (rows, each converter, products) out
-  // of the launch's.
+  // of the launch's.  Measured: d = 128, 2 x 1024 queries, 128 / 80 / 64 487 us,
+  // 136 / 72 / 64 474, 136 / 80 / 48 473, 144 / 80 / 32 479, 152 / 64 / 48 486;
+  // d = 256, 4096 queries, 208 / 104 / 96 1745 us, 232 / 112 / 56 1541,
+  // 224 / 120 / 48 1475, 232 / 120 / 40 1552 (the issuing warp's code is the
+  // better the less room it is given, down to 48).
   static constexpr int kLaunchRegs = kBlocks == 2 ? 96 : 128;
-  static constexpr int kRowRegs = kBlocks == 2 ? 128 : 208;
-  static constexpr int kConvRegs = kBlocks == 2 ? 80 : 104;
-  static constexpr int kMmaRegs = kBlocks == 2 ? 64 : 96;
+  static constexpr int kRowRegs = kBlocks == 2 ? 136 : 224;
+  static constexpr int kConvRegs = kBlocks == 2 ? 80 : 120;
+  static constexpr int kMmaRegs = 48;
   static_assert(kBlocks * kRowRegs + 2 * kConvRegs + kMmaRegs <= (kBlocks + 3) * kLaunchRegs, "register split");
 };
 
