@@ -755,3 +755,60 @@ def test_two_streams_of_chunks(fa):
         for (o, l), (o1, l1) in zip(alone, got):
             assert torch.equal(o, o1) and torch.equal(l, l1)
     fa.fa_check_error()
+
+
+@pytest.mark.parametrize("lens,nq", [([9000, 33], [1, 2]), ([200, 33], [1, 2]), ([1900, 600], [150, 20]), ([300, 64], [90, 64])])
+def test_a_workspace_may_hold_anything(fa, lens, nq):
+    import torch
+    c = attention_case(131, lens, nq, 2, 4, 128, 32, 64)
+    o, l = run_attention(fa, c)
+    compare(o, l, c)
+    size = fa.kv4_attention_workspace_bytes(8, 2, 128, max(nq))
+    for byte in (0, 255):
+        o1, l1 = run_attention(fa, c, workspace=torch.full((size,), byte, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(o, o1) and torch.equal(l, l1)
+    fa.fa_check_error()
+
+
+@pytest.mark.parametrize("d,nq", [(64, 1), (128, 5), (128, 90), (256, 40)])
+def test_lengths_past_the_table_are_clamped(fa, d, nq):
+    import torch
+    c = attention_case(141 + d, [640, 320], [nq, 1], 1, 4, d, 32, 64, table_pad=0)
+    c["table"][1, 5:] = c["table"][0, 5:]      # the table's rows are full
+    c["kv_len"] = np.asarray([640, 640], np.int32)
+    o, l = run_attention(fa, c)
+    compare(o, l, c)
+    for far in (641, 10**6, 2**31 - 1):
+        o1, l1 = run_attention(fa, dict(c, kv_len=np.asarray([far, far], np.int32)))
+        assert torch.equal(o, o1) and torch.equal(l, l1)
+    fa.fa_check_error()
+
+
+def test_calls_without_rows(fa):
+    import torch
+    cache = fa.kv4_cache(4, 2, 16, 64)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    fa.kv4_append(none, none, i32([]), cache, 16)
+    k, v = fa.kv4_gather(i32([]), cache, 16, 64)
+    assert k.shape == v.shape == (0, 2, 64)
+    table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    o, l = fa.kv4_attention(none, cache, table, i32([0, 0, 0]), i32([0, 0]), 1, 16)
+    assert o.shape == (0, 2, 64) and l.shape == (0, 2)
+    # rows, and no request that has any: nothing is written
+    q = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for max_q in (1, 300):
+        o, l = torch.full_like(q, 5.0), torch.full((3, 2), 5.0, device="cuda")
+        fa.kv4_attention(q, cache, table, i32([0, 0, 0]), i32([0, 0]), max_q, 16, out=o, lse=l)
+        assert (o == 5).all() and (l == 5).all()
+    fa.fa_check_error()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_bound_on_queries_only_chooses_the_kernel(fa, d):
+    # one query a request, told it might be many: every block of rows, cut and whole
+    for lens in ([700, 5, 129], [5000, 64, 1]):
+        c = attention_case(d + lens[0], lens, [1, 1, 1], 2, 2, d, 32, 32)
+        for max_q in (1, 4, 5, 8, 12, 16, 24, 33, 64, 5000):
+            o, l = run_attention(fa, c, max_q=max_q)
+            compare(o, l, c)
+    fa.fa_check_error()
