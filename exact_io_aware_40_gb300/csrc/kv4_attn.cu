@@ -723,10 +723,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 
 // Joins the parts of the items that shares' ends cut: one warp per row.  The
 // order of the sums is that of the parts, so the result does not depend on
-// which CTA ran when.  Bound by latency: the record, the parts' statistics
-// (a lane each) and their rows (independent loads) are the three round trips.
+// which CTA ran when.  Bound by latency: the record, then the parts' statistics
+// (a lane each) and as many of their rows as registers hold, side by side.
 constexpr int kMergeWarps = 8;
-template <int HD>
+template <int HD, bool kMany>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     kv4_merge_kernel(const Kv4AttnArgs a, int block_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -740,38 +740,60 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   auto place = [&](int p) {  // part p: this CTA's last item, then its successors' first
     return (p == 0 ? 2ll * first + 1 : 2ll * (first + p)) * block_rows + row;
   };
+  // A row is HD / 4 float4: at d = 64 the half-warps take every other part.
+  constexpr int kSide = HD == 64 ? 2 : 1, kVec = HD == 256 ? 2 : 1;
+  // Rows of parts in flight.  With few rows an item may have dozens of parts (101
+  // -> 96 us for three requests of up to 128K tokens); with many it has a
+  // few, and registers for 16 would keep blocks from starting (473 -> 490 us).
+  constexpr int kFly = kMany ? 4 : HD == 256 ? 8 : 16;
+  const int side = HD == 64 ? lane >> 4 : 0, quad = HD == 64 ? lane & 15 : lane;
+  float4 y[kFly][kVec];
+  auto load = [&](int p) {  // volatile: issued here
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const float4* src =
+          reinterpret_cast<const float4*>(a.part_o + place(min(p + kSide * i + side, parts - 1)) * HD) + quad;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (p + kSide * i < parts)
+          asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(y[i][k].x), "=f"(y[i][k].y), "=f"(y[i][k].z), "=f"(y[i][k].w)
+                       : "l"(src + 32 * k));
+        else
+          y[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
   float2 st = make_float2(-INFINITY, 0.f);  // of part `lane`
   if (lane < parts) st = a.part_stat[place(lane)];
+  load(0);
   float top = st.x;
   for (int p = lane + 32; p < parts; p += 32) top = fmaxf(top, a.part_stat[place(p)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  // A row is HD / 4 float4: at d = 64 the half-warps take every other part.
-  constexpr int kSide = HD == 64 ? 2 : 1, kVec = HD == 256 ? 2 : 1;
-  const int side = HD == 64 ? lane >> 4 : 0, quad = HD == 64 ? lane & 15 : lane;
   float4 x[kVec];
 #pragma unroll
   for (int k = 0; k < kVec; ++k) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    const int n = min(parts - p0, 32);
-    if (p0 > 0) st = lane < n ? a.part_stat[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
-    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
-    l += st.y * f;
-#pragma unroll 16
-    for (int p = 0; p < n; p += kSide) {
-      const float g = __shfl_sync(0xffffffffu, f, p + side);  // 0 behind the last part
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + place(p0 + min(p + side, n - 1)) * HD);
+  float l = 0.f, f = 0.f;
+#pragma unroll 1
+  for (int p = 0; p < parts; p += kFly * kSide) {
+    if (p > 0) load(p);
+    if ((p & 31) == 0) {
+      if (p > 0) st = p + lane < parts ? a.part_stat[place(p + lane)] : make_float2(-INFINITY, 0.f);
+      f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+      l += st.y * f;
+    }
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        const float4 y = src[quad + 32 * k];
-        if (p + side < n) {
-          x[k].x = fmaf(y.x, g, x[k].x);
-          x[k].y = fmaf(y.y, g, x[k].y);
-          x[k].z = fmaf(y.z, g, x[k].z);
-          x[k].w = fmaf(y.w, g, x[k].w);
+    for (int i = 0; i < kFly; ++i) {
+      const int q = p + kSide * i + side;
+      const float g = __shfl_sync(0xffffffffu, f, q & 31);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (q < parts) {
+          x[k].x = fmaf(y[i][k].x, g, x[k].x);
+          x[k].y = fmaf(y[i][k].y, g, x[k].y);
+          x[k].z = fmaf(y[i][k].z, g, x[k].z);
+          x[k].w = fmaf(y[i][k].w, g, x[k].w);
         }
-      }
     }
   }
 #pragma unroll
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   if (lane == 0) a.L[o] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2f;
 }
 
-template <int HD>
+template <int HD, bool kMany>
 cudaError_t launch_merge(const Kv4AttnArgs& a, int ctas, int block_rows, cudaStream_t stream) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -806,7 +828,7 @@ cudaError_t launch_merge(const Kv4AttnArgs& a, int ctas, int block_rows, cudaStr
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<HD>, a, block_rows);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<HD, kMany>, a, block_rows);
 }
 
 template <int HD, int GROUP, int NT>
@@ -835,7 +857,7 @@ cudaError_t launch_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   kv4_attn_kernel<HD, GROUP, NT><<<ctas, kAttnThreads, C::kSmem, stream>>>(ag);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.whole_items) return e;
-  return launch_merge<HD>(a, ctas, C::kRows, stream);
+  return launch_merge<HD, false>(a, ctas, C::kRows, stream);
 }
 
 template <int HD, int GROUP>
@@ -844,7 +866,7 @@ cudaError_t launch_attn_rows(const Kv4AttnArgs& a, cudaStream_t stream) {
   if (block >= 128) {
     int ctas = 0;
     const cudaError_t e = launch_kv4_chunk(HD, GROUP, a, stream, &ctas);
-    return e != cudaSuccess || a.whole_items ? e : launch_merge<HD>(a, ctas, block, stream);
+    return e != cudaSuccess || a.whole_items ? e : launch_merge<HD, true>(a, ctas, block, stream);
   }
   if (block == 8) return launch_attn<HD, GROUP, 1>(a, stream);
   if constexpr (HD <= 128)
