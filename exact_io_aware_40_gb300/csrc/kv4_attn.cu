@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<HD, GROUP, NT>::kMinCtas
 // order of the sums is that of the parts, so the result does not depend on
 // which CTA ran when.  Bound by latency: the record, then the parts' statistics
 // (a lane each) and as many of their rows as registers hold, side by side.
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
 template <int HD, bool kMany>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     kv4_merge_kernel(const Kv4AttnArgs a, int block_rows) {
@@ -742,10 +742,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   };
   // A row is HD / 4 float4: at d = 64 the half-warps take every other part.
   constexpr int kSide = HD == 64 ? 2 : 1, kVec = HD == 256 ? 2 : 1;
-  // Rows of parts in flight.  With few rows an item may have dozens of parts (101
-  // -> 96 us for three requests of up to 128K tokens); with many it has a
-  // few, and registers for 16 would keep blocks from starting (473 -> 490 us).
-  constexpr int kFly = kMany ? 4 : HD == 256 ? 8 : 16;
+  // Rows of parts in flight.  More registers keep blocks, most of which have
+  // nothing to do, from starting.  With few rows an item may have dozens of parts:
+  // 16 in flight 46.4 us (32 requests of up to 8K tokens) and 96.2 us (three of up
+  // to 128K), 8 45.2 and 94.3, 4 45.5 and 96.4.  With many rows it has a few: 16
+  // in flight 490 us where 4 take 472.
+  constexpr int kFly = kMany || HD == 256 ? 4 : 8;
   const int side = HD == 64 ? lane >> 4 : 0, quad = HD == 64 ? lane & 15 : lane;
   float4 y[kFly][kVec];
   auto load = [&](int p) {  // volatile: issued here
