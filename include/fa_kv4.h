@@ -123,8 +123,9 @@ fa_status fa_kv4_gather(const int32_t* slots, const void* cache, int num_pages, 
  * d is 64, 128 or 256.  A query that sees no key gets O = 0, L = -inf.  Rows of
  * O and L behind cu_q[B] are left as they were.  Deterministic.  Keys have to be
  * below 2^116 in size; a key or value that is NaN reaches the queries that see
- * it and no others.  Make a first call with the same d, group and max_q before
- * any stream capture (it may load device code).
+ * it and no others, and a query that is not finite its own row alone.  Requests
+ * may share pages.  Make a first call with the same d, group, max_q, max_pages
+ * and window before any stream capture (it may load device code).
  */
 size_t fa_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q);
 size_t fa_kv4_attn_call_workspace_bytes(int B, int total_q, int max_q, int Hq, int Hkv, int d,
