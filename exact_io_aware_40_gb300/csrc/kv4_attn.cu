@@ -33,7 +33,7 @@
 // at most (V).
 //
 // Measured (d = 128, 16 requests of 8192 tokens, 8 K/V heads, 8 query heads each):
-// 46 us for 168 MB of cache, of which 10 to 15 us are paid once a call (launch,
+// 44 us for 168 MB of cache, of which 10 to 13 us are paid once a call (launch,
 // shares, first copies, the exchange between warps, merge); in between 5.2 to 5.6
 // TB/s.  Bound: issue slots (57 % taken, with 16 warps an SM and each warp's chain
 // from codes to weights to hide), about 380 instructions for 16 tokens of a head.
@@ -888,11 +888,11 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // for many rows converts every tile once.
 // Measured in us for blocks of 8, 16, 32, many, with 16 requests of 8192 tokens
 // and with 64 of 768 (8 K/V heads at d = 128):
-//   d = 64   32 rows 169 123 108 224 |  94  73  71 142     d = 128   16 rows  77  73 154 |  43  40 103
-//            48      246 174 193 225 | 136 102 125 142               24      112 120 156 |  62  67 105
-//            64      324 228 194 226 | 177 127 127 143               48      208 170 157 | 110  97 107
-//            80      399 279 278 226 | 217 165 179 145               56      240 217 158 | 120 124 108
-//   d = 256  32 rows 136 (8), 164 (many) | 78, 91              40 rows 168, 164 | 95, 91
+//   d = 64   32 rows 167 121 108 223 |  93  72  72 140     d = 128   16 rows  76  70 161 |  43  39 101
+//            48      243 173 193 224 | 135 102 125 140               24      110 117 162 |  61  67 104
+//            64      321 225 195 225 | 176 126 127 141               48      206 167 164 | 110  97 105
+//            80      397 276 279 226 | 216 163 178 142               56      238 213 165 | 120 125 105
+//   d = 256  32 rows 135 (8), 146 (many) | 78, 84              40 rows 166, 146 | 94, 85
 int kv4_attn_rows(int d, int rows) {
   if (rows <= 8) return 8;
   if (d == 64) return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 16 : rows <= 64 ? 32 : 256;

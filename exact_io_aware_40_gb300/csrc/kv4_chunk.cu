@@ -29,8 +29,8 @@
 // fits the tile's largest param.  K's unit multiplies the tile's scores; V's goes
 // into the exponent of P, whose reference then includes the largest unit so far.
 //
-// Measured (d = 128, 2 x 1024 queries of 32 heads over 8K to 16K keys): 473 us,
-// 1024 TFLOP/s, 0.52 of the measured bf16 peak; a tile takes about 2300 clocks of
+// Measured (d = 128, 2 x 1024 queries of 32 heads over 8K to 16K keys): 472 us,
+// 1026 TFLOP/s, 0.52 of the measured bf16 peak; a tile takes about 2300 clocks of
 // which the products need 1100.  Bound: the rows' chain from S to P among the other
 // roles' instructions (2270 of 2880 clocks a tile in a build that counted; about
 // 17 instructions for eight codes, 3.5 for a score, 64 % of the issue slots).  A
